@@ -22,6 +22,8 @@ LWQ_Q8_0, LWQ_Q4_0, LWQ_Q4_K, LWQ_Q6_K, LWQ_Q5_K, LWQ_Q2_K = 1, 2, 3, 4, 5, 6
 LWQ_ACT_F32, LWQ_ACT_F16, LWQ_ACT_BF16 = 0x000, 0x100, 0x200
 LWQ_FLAG_OVERLAP = 0x1000   # weights constant: allow programmatic dependent launch
 LWQ_FLAG_ACT_I8 = 0x2000    # int8 activation blocks of 32 (integer block dot products)
+LWQ_FLAG_OUT16 = 0x4000     # paged attention: out in the cache's 16-bit type
+LWQ_ROPE_HALF, LWQ_ROPE_PAIRS = 0, 1
 LWQ_OK = 0
 LWQ_ERR_INVALID_ARG = 1
 LWQ_ERR_UNSUPPORTED = 2
@@ -30,9 +32,10 @@ LWQ_ERR_NOT_INITIALIZED = 4
 LWQ_ERR_WORKSPACE_TOO_SMALL = 5
 LWQ_ERR_CUDA = 6
 LWQ_ERR_DEVICE_TIMEOUT = 7
+LWQ_ERR_BAD_PAGE = 8
 STATUS = {0: "LWQ_OK", 1: "LWQ_ERR_INVALID_ARG", 2: "LWQ_ERR_UNSUPPORTED", 3: "LWQ_ERR_MISALIGNED",
           4: "LWQ_ERR_NOT_INITIALIZED", 5: "LWQ_ERR_WORKSPACE_TOO_SMALL", 6: "LWQ_ERR_CUDA",
-          7: "LWQ_ERR_DEVICE_TIMEOUT"}
+          7: "LWQ_ERR_DEVICE_TIMEOUT", 8: "LWQ_ERR_BAD_PAGE"}
 WEIGHT_FORMATS = {"q8_0": LWQ_Q8_0, "q4_0": LWQ_Q4_0, "q4_k": LWQ_Q4_K, "q6_k": LWQ_Q6_K, "q5_k": LWQ_Q5_K,
                   "q2_k": LWQ_Q2_K}
 ACT_DTYPES = {"f32": LWQ_ACT_F32, "f16": LWQ_ACT_F16, "bf16": LWQ_ACT_BF16}
@@ -41,7 +44,9 @@ ACT_DTYPES = {"f32": LWQ_ACT_F32, "f16": LWQ_ACT_F16, "bf16": LWQ_ACT_BF16}
 EXPORTS = ["lwq_row_bytes", "lwq_workspace_size", "lwq_init", "lwq_shutdown", "lwq_matmul",
            "lwq_select_config", "lwq_matmul_config", "lwq_status_string", "lwq_get_device_error",
            "lwq_selftest_timeout", "lwq_last_launch_count", "lwq_version", "lwq_matmul_noalloc",
-           "lwq_attention_workspace_size", "lwq_attention_decode"]
+           "lwq_attention_workspace_size", "lwq_attention_decode", "lwq_rope_init", "lwq_kv_append",
+           "lwq_attention_paged_workspace_size", "lwq_attention_paged",
+           "lwq_attention_prefill_workspace_size", "lwq_attention_prefill"]
 
 
 class LwqError(RuntimeError):
@@ -57,6 +62,29 @@ class lwq_config(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {f: getattr(self, f) for f, _ in self._fields_ if f != "reserved"}
+
+
+class lwq_paged(ctypes.Structure):
+    """The paged key/value cache and one batch of sequences (include/lwq.h).  Keeps the objects it was given
+    alive; the tensors' contents (page tables, lengths) may change between calls."""
+
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("tables", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("prefix_len", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("page", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int)]
+
+    def __init__(self, act: int, k, v, tables, lens, *, B: int, Hkv: int, D: int, page: int, max_pages: int,
+                 num_pages: int, prefix=None, prefix_len: int = 0):
+        super().__init__(_ptr(k), _ptr(v), _ptr(tables), _ptr(lens), _ptr(prefix), prefix_len, act, B, Hkv, D, page,
+                         max_pages, num_pages)
+        self.owners = (k, v, tables, lens, prefix)
+
+
+class lwq_rope(ctypes.Structure):
+    """The rotation of lwq_kv_append (include/lwq.h); filled by lwq_rope_init."""
+
+    _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("axes", ctypes.c_int),
+                ("reserved", ctypes.c_int), ("turn", ctypes.c_uint64 * 64), ("axis", ctypes.c_uint8 * 64)]
 
 
 def _load() -> ctypes.CDLL:
@@ -85,6 +113,19 @@ def _load() -> ctypes.CDLL:
     lib.lwq_attention_workspace_size.argtypes = [i, i, i, i, i]
     lib.lwq_attention_decode.restype = i
     lib.lwq_attention_decode.argtypes = [i, vp, vp, vp, vp, vp, i, i, i, i, i, c.c_float, vp]
+    pc, pr, i64 = c.POINTER(lwq_paged), c.POINTER(lwq_rope), c.c_int64
+    lib.lwq_rope_init.restype = i
+    lib.lwq_rope_init.argtypes = [pr, i, i, c.c_double, c.POINTER(c.c_double), i, c.POINTER(i)]
+    lib.lwq_kv_append.restype = i
+    lib.lwq_kv_append.argtypes = [pc, pr, i, vp, i64, vp, i64, vp, i64, vp, vp, vp, i, i, vp]
+    lib.lwq_attention_paged_workspace_size.restype = c.c_size_t
+    lib.lwq_attention_paged_workspace_size.argtypes = [pc, i]
+    lib.lwq_attention_paged.restype = i
+    lib.lwq_attention_paged.argtypes = [pc, i, vp, vp, i, c.c_float, vp]
+    lib.lwq_attention_prefill_workspace_size.restype = c.c_size_t
+    lib.lwq_attention_prefill_workspace_size.argtypes = [pc, i, i]
+    lib.lwq_attention_prefill.restype = i
+    lib.lwq_attention_prefill.argtypes = [pc, i, vp, vp, vp, i, i, c.c_float, vp]
     return lib
 
 
@@ -169,7 +210,7 @@ def lwq_matmul_config(fmt: int, Wq, x, y, M: int, N: int, K: int, cfg: lwq_confi
 
 
 def lwq_get_device_error() -> int:
-    """LWQ_OK, or LWQ_ERR_DEVICE_TIMEOUT (and clears it); synchronize first."""
+    """LWQ_OK, LWQ_ERR_DEVICE_TIMEOUT or LWQ_ERR_BAD_PAGE (and clears it); synchronize first."""
     return _lib.lwq_get_device_error()
 
 
@@ -200,3 +241,46 @@ def lwq_attention_decode(act: int, q, k, v, seq_lens, out, B: int, H: int, Hkv: 
     """Decode attention through the C ABI (act: LWQ_ACT_F16 or LWQ_ACT_BF16; seq_lens may be None)."""
     _check(_lib.lwq_attention_decode(act, _ptr(q), _ptr(k), _ptr(v), _ptr(seq_lens), _ptr(out), B, H, Hkv, Lmax, D,
                                      float(scale), _stream(stream)), "lwq_attention_decode")
+
+
+def lwq_rope_init(rot_dim: int, base: float = 10000.0, layout: int = LWQ_ROPE_HALF, inv_freq=None,
+                  sections=None) -> lwq_rope:
+    """A rotation of the first rot_dim elements of each head; sections: pairs per position axis (None: one axis);
+    inv_freq: rot_dim // 2 frequencies in place of base ** (-2 i / rot_dim)."""
+    if inv_freq is not None and len(inv_freq) != rot_dim // 2:
+        raise ValueError(f"inv_freq needs {rot_dim // 2} frequencies, not {len(inv_freq)}")
+    rope = lwq_rope()
+    freq = None if inv_freq is None else (ctypes.c_double * len(inv_freq))(*[float(f) for f in inv_freq])
+    sec = None if sections is None else (ctypes.c_int * len(sections))(*sections)
+    _check(_lib.lwq_rope_init(ctypes.byref(rope), rot_dim, layout, float(base), freq,
+                              1 if sections is None else len(sections), sec), "lwq_rope_init")
+    return rope
+
+
+def lwq_kv_append(cache: lwq_paged, rope, src: int, q, ldq: int, k, ldk: int, v, ldv: int, q_out, T: int, H: int,
+                  cu_tokens=None, positions=None, stream=None) -> None:
+    """Rotate q and k by position (rope None: not) and store k and v in the cache (see include/lwq.h)."""
+    _check(_lib.lwq_kv_append(ctypes.byref(cache), None if rope is None else ctypes.byref(rope), src, _ptr(q), ldq,
+                              _ptr(k), ldk, _ptr(v), ldv, _ptr(q_out), _ptr(cu_tokens), _ptr(positions), T, H,
+                              _stream(stream)), "lwq_kv_append")
+
+
+def lwq_attention_paged_workspace_size(cache: lwq_paged, H: int) -> int:
+    return _lib.lwq_attention_paged_workspace_size(ctypes.byref(cache), H)
+
+
+def lwq_attention_paged(cache: lwq_paged, q, out, H: int, scale: float, flags: int = 0, stream=None) -> None:
+    """Decode attention, one query token per sequence, over the paged cache and its shared prefix."""
+    _check(_lib.lwq_attention_paged(ctypes.byref(cache), flags, _ptr(q), _ptr(out), H, float(scale),
+                                    _stream(stream)), "lwq_attention_paged")
+
+
+def lwq_attention_prefill_workspace_size(cache: lwq_paged, T: int, H: int) -> int:
+    return _lib.lwq_attention_prefill_workspace_size(ctypes.byref(cache), T, H)
+
+
+def lwq_attention_prefill(cache: lwq_paged, q, out, cu_tokens, T: int, H: int, scale: float, flags: int = 0,
+                          stream=None) -> None:
+    """Causal attention of the batch's new tokens over the cache that already holds them."""
+    _check(_lib.lwq_attention_prefill(ctypes.byref(cache), flags, _ptr(q), _ptr(out), _ptr(cu_tokens), T, H,
+                                      float(scale), _stream(stream)), "lwq_attention_prefill")

@@ -19,6 +19,7 @@
 #include "lwq_gemv.cuh"
 #include "lwq_gemv_simple.cuh"
 #include "lwq_attn.cuh"
+#include "lwq_paged.cuh"
 
 namespace lwq {
 namespace {
@@ -905,6 +906,7 @@ const char *lwq_status_string(int s) {
     case LWQ_ERR_WORKSPACE_TOO_SMALL: return "workspace too small (see lwq_workspace_size)";
     case LWQ_ERR_CUDA: return "CUDA error";
     case LWQ_ERR_DEVICE_TIMEOUT: return "a kernel gave up a bounded wait";
+    case LWQ_ERR_BAD_PAGE: return "a page table held a page outside the cache";
     default: return "unknown status";
     }
 }
@@ -915,7 +917,7 @@ int lwq_get_device_error(void) {
     if (v == 0) return LWQ_OK;
     unsigned zero = 0;
     if (cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(zero)) != cudaSuccess) return LWQ_ERR_CUDA;
-    return LWQ_ERR_DEVICE_TIMEOUT;
+    return v == DEVERR_BAD_PAGE ? LWQ_ERR_BAD_PAGE : LWQ_ERR_DEVICE_TIMEOUT;
 }
 
 int lwq_selftest_timeout(unsigned timeout_us, void *stream) {
@@ -987,3 +989,6 @@ int lwq_version(void) { return 0x000100; }
 // library is one device module: one copy of each kernel and of the device
 // error word that every bounded wait sets.
 #include "lwq_noalloc.cuh"
+
+// So do the operators of the paged key/value cache.
+#include "lwq_paged_api.cuh"

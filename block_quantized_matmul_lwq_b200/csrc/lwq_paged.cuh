@@ -1,0 +1,267 @@
+// The paged key/value cache: appending to it with the rotation of positions,
+// and attention over it (see include/lwq.h, "paged key/value cache").
+//
+// Layout: pages [num_pages][Hkv][page][D], so that one page of one kv head is
+// a contiguous run of page * D elements and a sequence's keys of a head are
+// such runs, named by its row of the page table.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/lwq.h"
+#include "lwq_attn.cuh"
+
+namespace lwq {
+
+// The cache as the kernels see it (lwq_paged with the derived sizes).
+struct PagedArgs {
+    uint16_t *k, *v;
+    const int *tables, *lens, *prefix;
+    int prefix_len;
+    int B, Hkv, page, page_shift, max_pages, num_pages;
+};
+
+// The page that holds token j of a sequence (or of the prefix) with page list
+// `list`, or -1 for a page number outside the cache (reported, never followed).
+__device__ __forceinline__ int page_of(const PagedArgs &c, const int *list, int j) {
+    const int p = __ldg(list + (j >> c.page_shift));
+    if (p >= 0 && p < c.num_pages) return p;
+    set_dev_error(DEVERR_BAD_PAGE);
+    return -1;
+}
+
+// Element offset of token j's row within page p, kv head g.
+template <int D>
+__device__ __forceinline__ size_t cache_row(const PagedArgs &c, int p, int g, int j) {
+    return (((size_t)p * c.Hkv + g) * c.page + (j & (c.page - 1))) * D;
+}
+
+// ------------------------------------------------------------------ append
+// Rotation and append in one pass: every element of q, k and v is read once
+// and written once, so the kernel is bound by HBM for long prompts and by the
+// launch for single tokens.
+//
+// A group of D / 8 lanes takes one head of a token: 4 pairs per lane, i.e. 4 + 4
+// (HALF) or 8 (PAIRS) consecutive elements, so that each warp-wide access is
+// whole 128-byte lines; a warp takes APPEND_ITERS such rows of one token with
+// all their loads in flight before the first store, and its lanes' four
+// (cos, sin) are computed once for all of them.  Small row counts per warp keep
+// a single token spread over several warps (48 heads of 128: 6 warps).
+//
+// The angle position * f is kept in turns as a 64-bit fraction: the low 64 bits
+// of position * turn are the exact product modulo one turn, and their top 32
+// bits, as a signed fraction of a half turn, go to sincospi.  So a position of
+// 2^31 costs no accuracy (fp32 angles would be off by whole turns there), and
+// no 64-bit floating point is used.
+constexpr int APPEND_ITERS = 4;
+constexpr int APPEND_WARPS = 4;
+
+struct AppendArgs {
+    PagedArgs c;
+    const void *q, *k, *v;
+    long ldq, ldk, ldv;
+    uint16_t *q_out;
+    const int *cu, *positions;
+    int T, H, units;   // units: warps per token
+    int rope;          // 0: no rotation
+    int pairs_layout;  // LWQ_ROPE_PAIRS
+};
+
+// 4 consecutive elements of a row in fp32 (ST: the source type).
+template <int ST>
+__device__ __forceinline__ void load4(const void *row, int e, float (&f)[4]) {
+    if constexpr (ST == X_F32) {
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e));
+        f[0] = u.x;
+        f[1] = u.y;
+        f[2] = u.z;
+        f[3] = u.w;
+    } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + e));
+        f[0] = lo16<ST>(u.x);
+        f[1] = hi16<ST>(u.x);
+        f[2] = lo16<ST>(u.y);
+        f[3] = hi16<ST>(u.y);
+    }
+}
+template <int XT>
+__device__ __forceinline__ void store4(uint16_t *p, const float (&f)[4]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack16<XT>(f[0], f[1]), pack16<XT>(f[2], f[3]));
+}
+
+template <int ST, int XT, int D>
+__global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const AppendArgs a, const lwq_rope rope) {
+    constexpr int LPH = D / 8;          // lanes per head
+    constexpr int HPI = 32 / LPH;       // heads per warp access
+    const int lane = threadIdx.x & 31;
+    const long w = (long)blockIdx.x * APPEND_WARPS + (threadIdx.x >> 5);
+    const int t = (int)(w / a.units), unit = (int)(w % a.units);
+    if (t >= a.T) return;
+    const PagedArgs &c = a.c;
+    // the token's sequence b: the number of sequences that end at or before it
+    int b = t, idx = 0, n = 1;
+    if (a.cu) {
+        int cnt = 0;
+        for (int i = lane; i < c.B; i += 32) cnt += __ldg(a.cu + i + 1) <= t;
+        b = __reduce_add_sync(0xffffffffu, cnt);
+        if (b >= c.B) return;           // behind the last sequence
+        const int t0 = __ldg(a.cu + b);
+        idx = t - t0;
+        n = __ldg(a.cu + b + 1) - t0;
+    }
+    const long place = (long)__ldg(c.lens + b) - n + idx;
+    if (idx < 0 || idx >= n || place < 0) return;   // padding
+    const int pi = lane % LPH, sub = lane / LPH;
+    const bool turned = a.rope && 8 * pi < rope.rot_dim;
+    const bool halves = turned && !a.pairs_layout;
+    // element offsets of the lane's two groups of four
+    const int e0 = halves ? 4 * pi : 8 * pi;
+    const int e1 = halves ? e0 + rope.rot_dim / 2 : e0 + 4;
+    float cs[4], sn[4];
+    if (turned) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = a.positions ? __ldg(a.positions + (size_t)rope.axis[4 * pi + i] * a.T + t)
+                                      : c.prefix_len + (int)place;
+            const uint64_t turns = (uint64_t)(int64_t)p * rope.turn[4 * pi + i];
+            const int half_turns = (int)(uint32_t)((turns + 0x80000000ull) >> 32);
+            sincospif((float)half_turns * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31
+        }
+    }
+    int page = -1;
+    if (place < (long)c.max_pages * c.page)
+        page = page_of(c, c.tables + (size_t)b * c.max_pages, (int)place);
+    else
+        set_dev_error(DEVERR_BAD_PAGE);
+    const int hq = a.q ? a.H : 0, heads = hq + 2 * c.Hkv;
+    const int h0 = unit * APPEND_ITERS * HPI + sub;
+    float x[APPEND_ITERS][2][4];
+#pragma unroll
+    for (int i = 0; i < APPEND_ITERS; ++i) {
+        const int h = h0 + i * HPI;
+        if (h >= heads) break;
+        const long es = ST == X_F32 ? 4 : 2;
+        const char *row = h < hq ? static_cast<const char *>(a.q) + (t * a.ldq + (long)h * D) * es
+                        : h < hq + c.Hkv ? static_cast<const char *>(a.k) + (t * a.ldk + (long)(h - hq) * D) * es
+                                         : static_cast<const char *>(a.v) + (t * a.ldv + (long)(h - hq - c.Hkv) * D) * es;
+        // values, and elements the rotation leaves alone, go through the same two groups: a
+        // value row is read at the offsets of the rotation too (they cover the head all the same)
+        load4<ST>(row, e0, x[i][0]);
+        load4<ST>(row, e1, x[i][1]);
+    }
+#pragma unroll
+    for (int i = 0; i < APPEND_ITERS; ++i) {
+        const int h = h0 + i * HPI;
+        if (h >= heads) break;
+        uint16_t *dst;
+        if (h < hq) {
+            dst = a.q_out + ((size_t)t * a.H + h) * D;
+        } else {
+            if (page < 0) continue;
+            const bool key = h < hq + c.Hkv;
+            dst = (key ? c.k : c.v) + cache_row<D>(c, page, h - hq - (key ? 0 : c.Hkv), (int)place);
+        }
+        float(&u)[4] = x[i][0];
+        float(&v)[4] = x[i][1];
+        if (turned && h < hq + c.Hkv) {
+            if (a.pairs_layout) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float p = u[2 * j], r = u[2 * j + 1];
+                    u[2 * j] = p * cs[j] - r * sn[j];
+                    u[2 * j + 1] = r * cs[j] + p * sn[j];
+                    const float s = v[2 * j], z = v[2 * j + 1];
+                    v[2 * j] = s * cs[j + 2] - z * sn[j + 2];
+                    v[2 * j + 1] = z * cs[j + 2] + s * sn[j + 2];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = u[j], r = v[j];
+                    u[j] = p * cs[j] - r * sn[j];
+                    v[j] = r * cs[j] + p * sn[j];
+                }
+            }
+        }
+        store4<XT>(dst + e0, u);
+        store4<XT>(dst + e1, v);
+    }
+}
+
+// --------------------------------------------------------------- attention
+struct PagedAttnArgs {
+    PagedArgs c;
+    const uint16_t *q;
+    void *out;
+    const int *cu;      // null: one query per sequence
+    int T, H, G, causal;
+    int out16;
+    float qscale;       // scale * log2(e)
+};
+
+// One warp per (token, query head): the running maximum and sum over the keys
+// that the token sees, one key at a time.
+template <int XT, int D>
+__global__ void __launch_bounds__(128) paged_attn_rows_kernel(const PagedAttnArgs a) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long w = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int t = (int)(w / a.H), h = (int)(w % a.H), g = h / a.G;
+    if (t >= a.T) return;
+    const PagedArgs &c = a.c;
+    int b = t, idx = 0, n = 1;
+    if (a.cu) {
+        int cnt = 0;
+        for (int i = lane; i < c.B; i += 32) cnt += __ldg(a.cu + i + 1) <= t;
+        b = __reduce_add_sync(0xffffffffu, cnt);
+        if (b >= c.B) return;
+        const int t0 = __ldg(a.cu + b);
+        idx = t - t0;
+        n = __ldg(a.cu + b + 1) - t0;
+        if (idx < 0 || idx >= n) return;
+    }
+    const long cap = (long)c.max_pages * c.page;
+    const long place = (long)__ldg(c.lens + b) - n + idx;
+    const int own = (int)(place + 1 < 0 ? 0 : place + 1 > cap ? cap : place + 1);
+    const int pre = place < 0 && a.causal ? 0 : c.prefix_len;
+    float qf[E], acc[E], m = -INFINITY, l = 0.f;
+    load_row<XT, E>(a.q + ((size_t)t * a.H + h) * D + E * lane, qf);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int j = 0; j < pre + own; ++j) {
+        const int jj = j < pre ? j : j - pre;
+        const int p = page_of(c, j < pre ? c.prefix : c.tables + (size_t)b * c.max_pages, jj);
+        float kf[E], vf[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) kf[e] = vf[e] = 0.f;
+        if (p >= 0) {
+            load_row<XT, E>(c.k + cache_row<D>(c, p, g, jj) + E * lane, kf);
+            load_row<XT, E>(c.v + cache_row<D>(c, p, g, jj) + E * lane, vf);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s = fmaf(qf[e], kf[e], s);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        s *= a.qscale;
+        const float mn = fmaxf(m, s), f = exp2f(m - mn), pr = exp2f(s - mn);
+        m = mn;
+        l = fmaf(l, f, pr);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, pr * vf[e]);
+    }
+    const float r = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const size_t at = ((size_t)t * a.H + h) * D + E * lane + e;
+        if (a.out16)
+            static_cast<uint16_t *>(a.out)[at] = (uint16_t)pack16<XT>(acc[e] * r, 0.f);
+        else
+            static_cast<float *>(a.out)[at] = acc[e] * r;
+    }
+}
+
+}  // namespace lwq

@@ -1,0 +1,279 @@
+// Host side of the paged key/value cache: argument checks, work division and
+// launches (see include/lwq.h).  Included by lwq_api.cu: the library is one
+// translation unit, with one copy of the device error word.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "../../include/lwq.h"
+#include "lwq_paged.cuh"
+
+namespace lwq {
+namespace {
+
+constexpr long kMaxIndex = 0x7fffffffl;
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes and types of the cache description alone (the workspace sizes need no pointers).
+int paged_sizes(const lwq_paged *c, int H) {
+    if (!c || c->B <= 0 || c->Hkv <= 0 || c->D <= 0 || c->page <= 0 || c->max_pages <= 0 || c->num_pages <= 0 ||
+        c->prefix_len < 0 || H <= 0)
+        return LWQ_ERR_INVALID_ARG;
+    if (c->dtype != LWQ_ACT_F16 && c->dtype != LWQ_ACT_BF16) return LWQ_ERR_UNSUPPORTED;
+    if (c->D != 64 && c->D != 128) return LWQ_ERR_UNSUPPORTED;
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return LWQ_ERR_UNSUPPORTED;
+    if (H % c->Hkv) return LWQ_ERR_INVALID_ARG;
+    if (H / c->Hkv > 16) return LWQ_ERR_UNSUPPORTED;
+    // token rows of the cache and places of a sequence are 32-bit numbers in the kernels
+    if ((double)c->num_pages * c->Hkv * c->page > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
+    if ((double)c->max_pages * c->page + c->prefix_len > (double)(kMaxIndex - 1024)) return LWQ_ERR_UNSUPPORTED;
+    if (c->B > 65535 || c->Hkv > 65535) return LWQ_ERR_UNSUPPORTED;
+    return LWQ_OK;
+}
+
+int paged_pointers(const lwq_paged *c) {
+    if (!c->k || !c->v || !c->tables || !c->lens || (c->prefix_len > 0 && !c->prefix)) return LWQ_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->tables) || !aligned4(c->lens) || !aligned4(c->prefix))
+        return LWQ_ERR_MISALIGNED;
+    return LWQ_OK;
+}
+
+PagedArgs paged_args(const lwq_paged *c) {
+    PagedArgs p;
+    p.k = static_cast<uint16_t *>(c->k);
+    p.v = static_cast<uint16_t *>(c->v);
+    p.tables = c->tables;
+    p.lens = c->lens;
+    p.prefix = c->prefix;
+    p.prefix_len = c->prefix_len;
+    p.B = c->B;
+    p.Hkv = c->Hkv;
+    p.page = c->page;
+    p.page_shift = 0;
+    while ((1 << p.page_shift) < c->page) ++p.page_shift;
+    p.max_pages = c->max_pages;
+    p.num_pages = c->num_pages;
+    return p;
+}
+
+// [a, a + an) and [b, b + bn) share a byte
+bool overlap(const void *a, size_t an, const void *b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bn && y < x + an;
+}
+
+int rope_check(const lwq_rope *r, int D) {
+    if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > D) return LWQ_ERR_UNSUPPORTED;
+    if (r->layout != LWQ_ROPE_HALF && r->layout != LWQ_ROPE_PAIRS) return LWQ_ERR_UNSUPPORTED;
+    if (r->axes < 1 || r->axes > 4) return LWQ_ERR_UNSUPPORTED;
+    for (int i = 0; i < r->rot_dim / 2; ++i)
+        if (r->axis[i] >= r->axes) return LWQ_ERR_INVALID_ARG;
+    return LWQ_OK;
+}
+
+template <int ST, int XT>
+cudaError_t launch_append(int D, const AppendArgs &a, const lwq_rope &rope, unsigned blocks, cudaStream_t st) {
+    if (D == 64)
+        kv_append_kernel<ST, XT, 64><<<blocks, APPEND_WARPS * 32, 0, st>>>(a, rope);
+    else
+        kv_append_kernel<ST, XT, 128><<<blocks, APPEND_WARPS * 32, 0, st>>>(a, rope);
+    return cudaGetLastError();
+}
+template <int ST>
+cudaError_t launch_append_xt(int dtype, int D, const AppendArgs &a, const lwq_rope &rope, unsigned blocks,
+                             cudaStream_t st) {
+    return dtype == LWQ_ACT_F16 ? launch_append<ST, X_F16>(D, a, rope, blocks, st)
+                                : launch_append<ST, X_BF16>(D, a, rope, blocks, st);
+}
+
+// The checks that both attention calls make, and the kernels' view of the arguments.
+int paged_attn_args(const lwq_paged *c, int flags, const void *q, void *out, const int32_t *cu, int T, int H,
+                    float scale, int causal, PagedAttnArgs *a) {
+    int rc = paged_sizes(c, H);
+    if (rc) return rc;
+    if (T <= 0 || !q || !out || (!cu && T != c->B) || !isfinite(scale)) return LWQ_ERR_INVALID_ARG;
+    if ((rc = paged_pointers(c))) return rc;
+    if (flags & ~LWQ_FLAG_OUT16) return LWQ_ERR_UNSUPPORTED;
+    if ((double)T * H > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(out) || !aligned4(cu)) return LWQ_ERR_MISALIGNED;
+    a->c = paged_args(c);
+    a->q = static_cast<const uint16_t *>(q);
+    a->out = out;
+    a->cu = cu;
+    a->T = T;
+    a->H = H;
+    a->G = H / c->Hkv;
+    a->causal = causal;
+    a->out16 = (flags & LWQ_FLAG_OUT16) ? 1 : 0;
+    a->qscale = scale * 1.4426950408889634f;   // log2(e): the kernels take exponentials as exp2
+    return LWQ_OK;
+}
+
+int paged_workspace(int dev, size_t need, void **ws) {
+    *ws = nullptr;
+    if (need == 0) return LWQ_OK;
+    if (!g_dev[dev].registered) return LWQ_ERR_NOT_INITIALIZED;
+    if (g_dev[dev].ws_bytes < need) return LWQ_ERR_WORKSPACE_TOO_SMALL;
+    *ws = g_dev[dev].ws;
+    return LWQ_OK;
+}
+
+cudaError_t launch_rows(int dtype, int D, const PagedAttnArgs &a, cudaStream_t st) {
+    const unsigned blocks = (unsigned)(((long)a.T * a.H + 3) / 4);
+    if (dtype == LWQ_ACT_F16)
+        D == 64 ? paged_attn_rows_kernel<X_F16, 64><<<blocks, 128, 0, st>>>(a)
+                : paged_attn_rows_kernel<X_F16, 128><<<blocks, 128, 0, st>>>(a);
+    else
+        D == 64 ? paged_attn_rows_kernel<X_BF16, 64><<<blocks, 128, 0, st>>>(a)
+                : paged_attn_rows_kernel<X_BF16, 128><<<blocks, 128, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace lwq
+
+extern "C" {
+
+int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const double *inv_freq, int axes,
+                  const int *sections) {
+    if (!rope || (!sections && axes != 1)) return LWQ_ERR_INVALID_ARG;
+    if (rot_dim < 16 || rot_dim > 128 || rot_dim % 16 || axes < 1 || axes > 4 ||
+        (layout != LWQ_ROPE_HALF && layout != LWQ_ROPE_PAIRS))
+        return LWQ_ERR_UNSUPPORTED;
+    if (!inv_freq && !(isfinite(base) && base > 0)) return LWQ_ERR_INVALID_ARG;
+    const int half = rot_dim / 2;
+    lwq_rope r;
+    memset(&r, 0, sizeof(r));
+    r.rot_dim = rot_dim;
+    r.layout = layout;
+    r.axes = axes;
+    int at = 0;
+    for (int a = 0; a < axes; ++a) {
+        const int n = sections ? sections[a] : half;
+        if (n < 0 || n > half - at) return LWQ_ERR_INVALID_ARG;
+        for (int i = 0; i < n; ++i) r.axis[at++] = (uint8_t)a;
+    }
+    if (at != half) return LWQ_ERR_INVALID_ARG;
+    const long double two_pi = 6.283185307179586476925286766559006L;
+    for (int i = 0; i < half; ++i) {
+        const long double f = inv_freq ? (long double)inv_freq[i] : powl((long double)base, -2.0L * i / rot_dim);
+        if (!isfinite(f) || fabsl(f) > 1048576.0L) return LWQ_ERR_INVALID_ARG;
+        long double t = f / two_pi;
+        t -= floorl(t);
+        const long double u = ldexpl(t, 64);   // in [0, 2^64]: a fraction that rounded up to 1 is 0 turns
+        r.turn[i] = u >= 18446744073709551615.0L ? 0 : (uint64_t)u;
+    }
+    *rope = r;
+    return LWQ_OK;
+}
+
+int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const void *q, int64_t ldq, const void *k,
+                  int64_t ldk, const void *v, int64_t ldv, void *q_out, const int32_t *cu_tokens,
+                  const int32_t *positions, int T, int H, void *stream) {
+    t_last_launches = 0;
+    int rc = paged_sizes(cache, H);
+    if (rc) return rc;
+    if (T <= 0 || !k || !v || !q != !q_out || (!cu_tokens && T != cache->B)) return LWQ_ERR_INVALID_ARG;
+    if ((rc = paged_pointers(cache))) return rc;
+    const int D = cache->D;
+    if (src != LWQ_ACT_F32 && src != LWQ_ACT_F16 && src != LWQ_ACT_BF16) return LWQ_ERR_UNSUPPORTED;
+    if (rope && (rc = rope_check(rope, D))) return rc;
+    if ((q && ldq < (int64_t)H * D) || ldk < (int64_t)cache->Hkv * D || ldv < (int64_t)cache->Hkv * D)
+        return LWQ_ERR_INVALID_ARG;
+    const int64_t es = src == LWQ_ACT_F32 ? 4 : 2, big = (int64_t)1 << 40;
+    if ((q && ldq > big) || ldk > big || ldv > big) return LWQ_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned4(cu_tokens) ||
+        !aligned4(positions) || (q && ldq * es % 16) || ldk * es % 16 || ldv * es % 16)
+        return LWQ_ERR_MISALIGNED;
+    if (q) {
+        const size_t n = (size_t)T * H * D * 2;
+        if (overlap(q_out, n, q, ((size_t)(T - 1) * ldq + (size_t)H * D) * es) ||
+            overlap(q_out, n, k, ((size_t)(T - 1) * ldk + (size_t)cache->Hkv * D) * es) ||
+            overlap(q_out, n, v, ((size_t)(T - 1) * ldv + (size_t)cache->Hkv * D) * es))
+            return LWQ_ERR_INVALID_ARG;
+    }
+    int dev;
+    if ((rc = current_device(&dev))) return rc;
+    AppendArgs a;
+    a.c = paged_args(cache);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.cu = cu_tokens;
+    a.positions = positions;
+    a.T = T;
+    a.H = H;
+    const int per = APPEND_ITERS * (256 / D);   // heads per warp
+    a.units = ((q ? H : 0) + 2 * cache->Hkv + per - 1) / per;
+    const double warps = (double)T * a.units;
+    if (warps > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
+    a.rope = rope ? 1 : 0;
+    a.pairs_layout = rope && rope->layout == LWQ_ROPE_PAIRS;
+    lwq_rope r;
+    if (rope)
+        r = *rope;
+    else
+        memset(&r, 0, sizeof(r));
+    const unsigned blocks = (unsigned)(((long)T * a.units + APPEND_WARPS - 1) / APPEND_WARPS);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (src == LWQ_ACT_F32)
+        e = launch_append_xt<X_F32>(cache->dtype, D, a, r, blocks, st);
+    else if (src == LWQ_ACT_F16)
+        e = launch_append_xt<X_F16>(cache->dtype, D, a, r, blocks, st);
+    else
+        e = launch_append_xt<X_BF16>(cache->dtype, D, a, r, blocks, st);
+    if (e != cudaSuccess) return LWQ_ERR_CUDA;
+    t_last_launches = 1;
+    return LWQ_OK;
+}
+
+size_t lwq_attention_paged_workspace_size(const lwq_paged *cache, int H) {
+    if (paged_sizes(cache, H)) return 0;
+    return 256;
+}
+
+int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *out, int H, float scale,
+                        void *stream) {
+    t_last_launches = 0;
+    PagedAttnArgs a;
+    int rc = paged_attn_args(cache, flags, q, out, nullptr, cache ? cache->B : 0, H, scale, 0, &a);
+    if (rc) return rc;
+    int dev;
+    if ((rc = current_device(&dev))) return rc;
+    void *ws;
+    if ((rc = paged_workspace(dev, lwq_attention_paged_workspace_size(cache, H), &ws))) return rc;
+    if (launch_rows(cache->dtype, cache->D, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return LWQ_ERR_CUDA;
+    t_last_launches = 1;
+    return LWQ_OK;
+}
+
+size_t lwq_attention_prefill_workspace_size(const lwq_paged *cache, int T, int H) {
+    if (paged_sizes(cache, H) || T <= 0) return 0;
+    return 256;
+}
+
+int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void *out, const int32_t *cu_tokens,
+                          int T, int H, float scale, void *stream) {
+    t_last_launches = 0;
+    PagedAttnArgs a;
+    int rc = paged_attn_args(cache, flags, q, out, cu_tokens, T, H, scale, 1, &a);
+    if (rc) return rc;
+    int dev;
+    if ((rc = current_device(&dev))) return rc;
+    if (launch_rows(cache->dtype, cache->D, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return LWQ_ERR_CUDA;
+    t_last_launches = 1;
+    return LWQ_OK;
+}
+
+}  // extern "C"

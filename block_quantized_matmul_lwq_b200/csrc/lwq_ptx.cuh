@@ -18,6 +18,8 @@ enum : unsigned {
     DEVERR_GEMM_WAIT = 2u,
     DEVERR_SPLITK_WAIT = 4u,
     DEVERR_SELFTEST = 8u,
+    DEVERR_BAD_PAGE = 16u,    // a page table entry outside the cache (not a wait)
+    DEVERR_ATTN_WAIT = 32u,
 };
 
 // One copy per CUDA module (each .cu file of the library is its own module).

@@ -46,7 +46,8 @@ typedef enum {
     LWQ_ERR_NOT_INITIALIZED = 4,    /* a call needs the workspace and lwq_init was not called on this device */
     LWQ_ERR_WORKSPACE_TOO_SMALL = 5,/* the registered workspace is smaller than this call needs */
     LWQ_ERR_CUDA = 6,               /* a CUDA runtime/driver call failed (launch error, bad device) */
-    LWQ_ERR_DEVICE_TIMEOUT = 7      /* a kernel gave up a bounded wait (see lwq_get_device_error) */
+    LWQ_ERR_DEVICE_TIMEOUT = 7,     /* a kernel gave up a bounded wait (see lwq_get_device_error) */
+    LWQ_ERR_BAD_PAGE = 8            /* a page table held a page outside the cache (see lwq_get_device_error) */
 } lwq_status;
 
 /* ------------------------------------------------- format and dtype codes
@@ -241,6 +242,136 @@ size_t lwq_attention_workspace_size(int B, int H, int Hkv, int Lmax, int D);
 int lwq_attention_decode(int dtype, const void *q, const void *k, const void *v, const int32_t *seq_lens, float *out,
                          int B, int H, int Hkv, int Lmax, int D, float scale, void *stream);
 
+/* ------------------------------------------------------ paged key/value cache
+ * The operators between the qkv projection and the output projection of a
+ * serving step, over one cache that many sequences share:
+ *   lwq_kv_append           rotate q and k by position, store k and v
+ *   lwq_attention_paged     one query token per sequence (decode), with the
+ *                           tokens that all sequences begin with read once
+ *   lwq_attention_prefill   several new tokens per sequence, causally
+ *
+ * lwq_paged describes the cache and one batch of sequences:
+ *   k, v       [num_pages][Hkv][page][D] in dtype, 16-byte aligned
+ *   tables     [B][max_pages] int32, device: the page of tokens page * i ..
+ *              page * i + page - 1 of each sequence.  Entries past a
+ *              sequence's length are not read.
+ *   lens       [B] int32, device: tokens of each sequence in the cache, those
+ *              that the call appends or attends with included, the shared
+ *              prefix not.  0 (or less) is an empty sequence, e.g. a padded
+ *              row of a captured batch.  The attention calls take a length
+ *              beyond max_pages * page as that.
+ *   prefix     [ceil(prefix_len / page)] int32, device: the pages of a prefix
+ *              that every sequence begins with (a system prompt); NULL with
+ *              prefix_len 0.  Token j of a sequence is then at position
+ *              prefix_len + j.
+ *   dtype      LWQ_ACT_F16 or LWQ_ACT_BF16, of the cache and of q
+ *   D          64 or 128;  page: 16, 32, 64, 128 or 256
+ * The caller owns all of it; the struct itself is read during the call only.
+ * A page number outside [0, num_pages) that a live token needs is never
+ * followed: its keys and values read as zeros, nothing is stored for it, and
+ * lwq_get_device_error then returns LWQ_ERR_BAD_PAGE.  Memory in pages behind
+ * a sequence's last token may hold anything, NaN included. */
+typedef struct {
+    void *k, *v;
+    const int32_t *tables;
+    const int32_t *lens;
+    const int32_t *prefix;
+    int prefix_len;
+    int dtype;
+    int B, Hkv, D, page, max_pages, num_pages;
+} lwq_paged;
+
+/* Rotary positions.  Pair i of a head (i < rot_dim / 2) turns by the angle
+ * position[axis(i)] * f_i:  (a, b) -> (a cos - b sin, b cos + a sin); the
+ * elements from rot_dim on stay.
+ *   LWQ_ROPE_HALF   pair i is elements (i, i + rot_dim / 2)
+ *   LWQ_ROPE_PAIRS  pair i is elements (2 i, 2 i + 1)
+ * Angles are kept as 64-bit fractions of a full turn, so that the product
+ * with any 32-bit position is reduced exactly (cos and sin to about 2^-23,
+ * however far the position). */
+#define LWQ_ROPE_HALF 0
+#define LWQ_ROPE_PAIRS 1
+typedef struct {
+    int rot_dim, layout, axes, reserved;
+    uint64_t turn[64];      /* f_i / (2 pi) modulo 1, in units of 2^-64 */
+    uint8_t axis[64];
+} lwq_rope;
+
+/* Fill *rope on the host (once; it holds no pointers and may be copied).
+ *   rot_dim   a multiple of 16, 16 .. 128
+ *   f_i       inv_freq[i] (rot_dim / 2 finite doubles below 2^20 in size), or,
+ *             with inv_freq NULL, base^(-2 i / rot_dim), base > 0
+ *   axes      1 .. 4 position axes (3 for time, height and width); sections:
+ *             how many consecutive pairs each axis turns, rot_dim / 2 in all
+ *             (NULL with one axis)
+ * Errors: LWQ_ERR_INVALID_ARG, LWQ_ERR_UNSUPPORTED (rot_dim, layout, axes). */
+int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const double *inv_freq, int axes,
+                  const int *sections);
+
+/* Append the k and v of T tokens to the cache, and rotate q and k on the way.
+ *   rope       NULL: nothing is rotated
+ *   src        LWQ_ACT_F32, _F16 or _BF16: the type of q, k and v (fp32 is
+ *              what lwq_matmul writes)
+ *   q          T rows of H heads, ldq elements from row to row; k, v: T rows
+ *              of Hkv heads, ldk and ldv apart.  (One fused projection y of
+ *              [T][(H + 2 Hkv) D]: q = y, k = y + H D, v = y + (H + Hkv) D,
+ *              all three strides (H + 2 Hkv) D.)
+ *   q_out      [T][H][D] in the cache's dtype; may not overlap the inputs.
+ *              q and q_out may both be NULL: keys and values only.
+ *   cu_tokens  [B + 1] int32, device, ascending from 0: sequence b's tokens
+ *              are cu_tokens[b] .. cu_tokens[b + 1] - 1, the last ones of its
+ *              lens[b] tokens.  NULL: one token per sequence (T == B).
+ *   positions  [axes][T] int32, device, any values; NULL: prefix_len + the
+ *              token's place among its sequence's lens[b], on every axis
+ * Arithmetic is fp32, each result rounded once to nearest (so a value past
+ * fp16's range becomes infinite there).  Tokens from cu_tokens[B] on, and
+ * tokens whose place in the cache would be negative (lens[b] 0), are padding:
+ * nothing is read or written for them.  A place beyond max_pages * page is
+ * reported as LWQ_ERR_BAD_PAGE and its k and v are dropped.  Two tokens of a
+ * call may not share a place in the cache.  One kernel, no workspace.
+ * Errors: LWQ_ERR_INVALID_ARG (sizes, NULL pointers, T != B without
+ * cu_tokens, a stride below its row, q_out over an input), LWQ_ERR_UNSUPPORTED
+ * (types, D, page, H / Hkv > 16, rot_dim > D, sizes past 31 bits),
+ * LWQ_ERR_MISALIGNED (pointers or row strides that are not 16-byte multiples;
+ * index arrays: 4 bytes), LWQ_ERR_CUDA. */
+int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const void *q, int64_t ldq, const void *k,
+                  int64_t ldk, const void *v, int64_t ldv, void *q_out, const int32_t *cu_tokens,
+                  const int32_t *positions, int T, int H, void *stream);
+
+/* Flag of the two attention calls below: out in the cache's 16-bit type,
+ * rounded once, instead of fp32. */
+#define LWQ_FLAG_OUT16 0x4000
+
+/* Decode attention over the paged cache: q [B][H][D] in the cache's dtype,
+ * out [B][H][D] fp32 (or 16-bit, flags above).  Query h reads kv head
+ * h / (H / Hkv), H / Hkv at most 16.  With s_j = scale * (q . k_j) over the
+ * prefix_len + lens[b] tokens of sequence b,  out = sum_j softmax(s)_j v_j;
+ * a sequence with no token at all gets zeros.  The prefix's keys and values
+ * are read once for the whole batch, as one matrix product over all B queries.
+ * Needs the workspace of lwq_init: lwq_attention_paged_workspace_size bytes,
+ * which depends on the sizes in *cache (its pointers are not read) and never
+ * on the sequences' lengths.  lwq_attention_paged_workspace_size returns 0
+ * for invalid sizes.  Errors as lwq_kv_append's, LWQ_ERR_INVALID_ARG for a
+ * scale that is not finite, LWQ_ERR_NOT_INITIALIZED and
+ * LWQ_ERR_WORKSPACE_TOO_SMALL. */
+size_t lwq_attention_paged_workspace_size(const lwq_paged *cache, int H);
+int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *out, int H, float scale,
+                        void *stream);
+
+/* Causal attention of several new tokens per sequence over the cache that
+ * already holds them (call lwq_kv_append first): q and out [T][H][D], the
+ * tokens of sequence b at cu_tokens[b] .. cu_tokens[b + 1] - 1 (NULL: one
+ * each, T == B).  The token at place j of its sequence (0 .. lens[b] - 1)
+ * sees the prefix and the tokens 0 .. j.  A token that sees nothing gets
+ * zeros; rows from cu_tokens[B] on are left as they were.  The values of the
+ * sequence's own tokens must be finite: a token's probability of 0 for a
+ * later one multiplies its value.  Workspace and errors as
+ * lwq_attention_paged; it is needed only when few tokens meet long caches
+ * and the keys are split. */
+size_t lwq_attention_prefill_workspace_size(const lwq_paged *cache, int T, int H);
+int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void *out, const int32_t *cu_tokens,
+                          int T, int H, float scale, void *stream);
+
 /* ------------------------------------------------ errors and diagnostics */
 
 /* Static description of a status code. */
@@ -249,9 +380,11 @@ const char *lwq_status_string(int status);
 /* Device-side error word of the current device: every wait in the kernels
  * (on an mbarrier or a TMEM handoff) is bounded, in lwq_matmul and
  * lwq_matmul_noalloc alike; a kernel
- * that gives up sets a bit here and returns instead of hanging.  The caller
- * must synchronize first.  Returns LWQ_OK, LWQ_ERR_DEVICE_TIMEOUT (and clears
- * the word), or LWQ_ERR_CUDA. */
+ * that gives up sets a bit here and returns instead of hanging.  The paged
+ * cache's kernels set another for a page number outside the cache.  The caller
+ * must synchronize first.  Returns LWQ_OK, LWQ_ERR_DEVICE_TIMEOUT or
+ * LWQ_ERR_BAD_PAGE (and clears the word; a timeout comes first), or
+ * LWQ_ERR_CUDA. */
 int lwq_get_device_error(void);
 
 /* Launch a one-CTA kernel on `stream` that waits on an mbarrier nothing ever
