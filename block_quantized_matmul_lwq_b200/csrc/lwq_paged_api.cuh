@@ -10,6 +10,7 @@
 
 #include "../../include/lwq.h"
 #include "lwq_paged.cuh"
+#include "lwq_paged_decode.cuh"
 
 namespace lwq {
 namespace {
@@ -133,6 +134,29 @@ cudaError_t launch_rows(int dtype, int D, const PagedAttnArgs &a, cudaStream_t s
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------------ decode
+constexpr int kDecodeCtasPerSm = 2;
+
+template <int XT, int D, int NG, int PARTS>
+cudaError_t launch_paged_decode(const PagedDecodeArgs &d, const PagedCombineArgs &k, cudaStream_t st) {
+    auto kern = paged_decode_kernel<XT, D, NG, PARTS>;
+    constexpr size_t smem = PagedDecodeSmem<D, NG>::TOTAL;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_k(kern, d.ctas, PD_WARPS * 32, smem, st, false, d)) != cudaSuccess) return e;
+    return launch_k(paged_combine_kernel<XT, D>, d.a.c.B * d.a.H, PC_THREADS, 0, st, true, k);
+}
+template <int XT, int D, int PARTS>
+cudaError_t launch_paged_decode_g(const PagedDecodeArgs &d, const PagedCombineArgs &k, cudaStream_t st) {
+    return d.a.G <= 8 ? launch_paged_decode<XT, D, 1, PARTS>(d, k, st) : launch_paged_decode<XT, D, 2, PARTS>(d, k, st);
+}
+// fp16's two parts of a probability hold 22 bits; bf16 takes a third part for an fp32 result
+template <int D>
+cudaError_t launch_paged_decode_x(int dtype, const PagedDecodeArgs &d, const PagedCombineArgs &k, cudaStream_t st) {
+    if (dtype == LWQ_ACT_F16) return launch_paged_decode_g<X_F16, D, 2>(d, k, st);
+    return d.a.out16 ? launch_paged_decode_g<X_BF16, D, 2>(d, k, st) : launch_paged_decode_g<X_BF16, D, 3>(d, k, st);
+}
+
 }  // namespace
 }  // namespace lwq
 
@@ -238,7 +262,10 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
 
 size_t lwq_attention_paged_workspace_size(const lwq_paged *cache, int H) {
     if (paged_sizes(cache, H)) return 0;
-    return 256;
+    int dev = 0, sms = 148;
+    if (current_device(&dev) == LWQ_OK) sms = sm_count(dev);
+    const size_t ps = part_stride(cache->D) * sizeof(float);
+    return (size_t)kDecodeCtasPerSm * sms * 2 * (H / cache->Hkv) * ps;
 }
 
 int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *out, int H, float scale,
@@ -251,9 +278,24 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
     if ((rc = current_device(&dev))) return rc;
     void *ws;
     if ((rc = paged_workspace(dev, lwq_attention_paged_workspace_size(cache, H), &ws))) return rc;
-    if (launch_rows(cache->dtype, cache->D, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return LWQ_ERR_CUDA;
-    t_last_launches = 1;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (cache->prefix_len > 0) {
+        if (launch_rows(cache->dtype, cache->D, a, st) != cudaSuccess) return LWQ_ERR_CUDA;
+        t_last_launches = 1;
+        return LWQ_OK;
+    }
+    PagedCombineArgs k;
+    PagedDecodeArgs &d = k.d;
+    d.a = a;
+    d.slots = static_cast<float *>(ws);
+    d.whole = nullptr;
+    d.ctas = kDecodeCtasPerSm * sm_count(dev);
+    k.prefix = nullptr;
+    k.splits = 0;
+    const cudaError_t e = cache->D == 64 ? launch_paged_decode_x<64>(cache->dtype, d, k, st)
+                                         : launch_paged_decode_x<128>(cache->dtype, d, k, st);
+    if (e != cudaSuccess) return LWQ_ERR_CUDA;
+    t_last_launches = 2;
     return LWQ_OK;
 }
 

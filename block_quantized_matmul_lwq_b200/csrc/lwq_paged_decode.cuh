@@ -1,0 +1,496 @@
+// Decode attention over the paged cache: one query token per sequence.
+//
+// Every key and value is read once per kv head, shared by its G = H / Hkv
+// query heads, so HBM bounds the pass (2 x 2 x D bytes and 4 G D operations
+// per key).  The keys of all (sequence, kv head) pairs are laid end to end as
+// units of 64 keys, and the CTAs of one resident wave take equal runs of units:
+// ragged lengths, a single long sequence and a large batch all fill the GPU,
+// and the host needs to know none of the lengths.  A run may begin or end
+// inside a pair; such a pair's partial results (running maximum, sum, weighted
+// values) go to the workspace and a second kernel merges them.
+//
+// Within a CTA each of the 4 warps takes 16 of a unit's 64 keys (one page, as
+// pages are at least 16 tokens) through its own cp.async ring, which runs
+// ahead across units and pairs: the tensor cores form S = Q K^T and O += P V
+// with mma.sync (m16n8k16), rows being the query heads.  The probabilities
+// enter as exact sums of 16-bit parts: hi in MMA rows 0..7 and lo in rows
+// 8..15 of one product; in bf16, whose two parts hold only 16 bits, a third
+// part in a product of its own when the result is wanted in fp32.
+#pragma once
+
+#include "lwq_paged.cuh"
+
+namespace lwq {
+
+constexpr int PD_WARPS = 4;
+constexpr int PD_UNIT = 64;     // keys of a unit: 16 per warp
+
+// floats of one partial result: m (log2 domain), l, two unused, acc[D]
+__host__ __device__ constexpr int part_stride(int D) { return D + 4; }
+
+// 16 bytes from global to shared, or zeros (the source is not read then)
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool live) {
+    const int n = live ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ int own_len(const PagedArgs &c, int b) {
+    const int len = __ldg(c.lens + b), cap = c.max_pages * c.page;
+    return len < 0 ? 0 : len > cap ? cap : len;
+}
+__device__ __forceinline__ int units_of(int len) { return (len + PD_UNIT - 1) / PD_UNIT; }
+
+// The division of `total` units over n CTAs: the first r take q + 1, the others q (none, with fewer units than CTAs).
+struct Runs {
+    long q, r;
+    __device__ __forceinline__ Runs(long total, int n) : q(total / n), r(total % n) {}
+    __device__ __forceinline__ long start(int i) const { return q * i + (i < r ? i : r); }
+    __device__ __forceinline__ int cta_of(long u) const {   // the CTA whose run holds unit u < total
+        const long head = r * (q + 1);
+        return (int)(u < head ? u / (q + 1) : r + (u - head) / q);
+    }
+};
+
+// Units per kv head before sequence b (returned to every thread), and of the
+// whole batch, by all threads of the block.
+__device__ __forceinline__ void units_before(const PagedArgs &c, int b, long *before, long *all) {
+    __shared__ long sb[32], sa[32];
+    long x = 0, y = 0;
+    for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+        const int n = units_of(own_len(c, i));
+        y += n;
+        if (i < b) x += n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        sb[threadIdx.x >> 5] = x;
+        sa[threadIdx.x >> 5] = y;
+    }
+    __syncthreads();
+    x = y = 0;
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
+        x += sb[i];
+        y += sa[i];
+    }
+    *before = x;
+    *all = y;
+}
+
+struct PagedDecodeArgs {
+    PagedAttnArgs a;
+    float *slots;       // [ctas][2][G] partial results of a CTA's first and last pair
+    float *whole;       // [B][H] results of pairs that one CTA finished, when a prefix is still to be added
+    int ctas;
+};
+
+// A place in the list of units: pair (b, g), unit `u` of the pair's `n`.
+struct UnitPos {
+    int b, g, u, n, len;
+};
+__device__ __forceinline__ void next_unit(const PagedArgs &c, UnitPos &p) {
+    if (++p.u < p.n) return;
+    p.u = 0;
+    if (++p.g < c.Hkv) return;
+    p.g = 0;
+    do {
+        if (++p.b >= c.B) {
+            p.n = 0;
+            return;
+        }
+        p.len = own_len(c, p.b);
+        p.n = units_of(p.len);
+    } while (p.n == 0);
+}
+
+template <int D, int NG>
+struct PagedDecodeSmem {
+    // two CTAs per SM: 6 tiles of 16 keys in flight per warp at D = 64, 3 (2 beside the second head group) at 128
+    static constexpr int STAGES = D == 64 ? (NG == 2 ? 4 : 6) : (NG == 2 ? 2 : 3);
+    static constexpr uint32_t ROWB = 2 * D, TILEB = 16 * ROWB, STAGEB = 2 * TILEB;
+    static constexpr size_t RING = (size_t)PD_WARPS * STAGES * STAGEB;
+    static constexpr size_t MERGE = (size_t)PD_WARPS * 8 * NG * (D + 2) * 4;
+    static constexpr size_t TOTAL = RING + MERGE + 64;   // and the scan's words
+};
+
+// NG: groups of 8 query heads (1 or 2); PARTS: 16-bit parts of a probability (2 or 3)
+template <int XT, int D, int NG, int PARTS>
+__global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const PagedDecodeArgs d) {
+    using SM = PagedDecodeSmem<D, NG>;
+    constexpr int ST = SM::STAGES, NCH = D / 8;
+    constexpr uint32_t ROWB = SM::ROWB, TILEB = SM::TILEB, STAGEB = SM::STAGEB;
+    extern __shared__ __align__(128) uint8_t dsm[];
+    // the scan's words, in the dynamic space (its limit is raised to all that a block may have)
+    long *const s_warp = reinterpret_cast<long *>(dsm + SM::RING + SM::MERGE);
+    long *const s_before = s_warp + PD_WARPS;
+    int *const s_b = reinterpret_cast<int *>(s_before + 1);
+    const PagedAttnArgs &a = d.a;
+    const PagedArgs &c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3, G = a.G;
+
+    // this CTA's run of units, and the sequence that it begins in: a scan of the lengths, each
+    // thread taking a run of sequences
+    const int per = (c.B + PD_WARPS * 32 - 1) / (PD_WARPS * 32);
+    const int b_lo = min(c.B, (int)threadIdx.x * per), b_hi = min(c.B, b_lo + per);
+    long mine = 0;
+    for (int i = b_lo; i < b_hi; ++i) mine += units_of(own_len(c, i));
+    long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    long all = 0, excl = incl - mine;
+#pragma unroll
+    for (int i = 0; i < PD_WARPS; ++i) {
+        if (i < warp) excl += s_warp[i];
+        all += s_warp[i];
+    }
+    const long total = all * c.Hkv;
+    const Runs runs(total, d.ctas);
+    const long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
+    if (u0 >= u1) return;
+    {
+        const long want = u0 / c.Hkv;   // unit per kv head: before(b) <= want < before(b + 1)
+        if (want >= excl && want < excl + mine) {
+            long at = excl;
+            for (int i = b_lo; i < b_hi; ++i) {
+                const int n = units_of(own_len(c, i));
+                if (want < at + n) {
+                    *s_b = i;
+                    *s_before = at;
+                    break;
+                }
+                at += n;
+            }
+        }
+    }
+    __syncthreads();
+    const int steps = (int)(u1 - u0);
+    UnitPos cur;
+    cur.b = *s_b;
+    cur.len = own_len(c, cur.b);
+    cur.n = units_of(cur.len);
+    {
+        const long rem = u0 - *s_before * c.Hkv;
+        cur.g = (int)(rem / cur.n);
+        cur.u = (int)(rem % cur.n);
+    }
+    UnitPos ahead = cur;    // the unit whose keys are fetched next, and their page (looked up a unit ahead)
+    auto lookup = [&](const UnitPos &p) {
+        const int j = p.u * PD_UNIT + 16 * warp;
+        return p.n > 0 && j < p.len ? __ldg(c.tables + (size_t)p.b * c.max_pages + (j >> c.page_shift)) : -1;
+    };
+    int page = lookup(ahead);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dsm) + (uint32_t)warp * ST * STAGEB;
+    auto issue = [&](int i) {
+        if (i < steps) {
+            const int j0 = ahead.u * PD_UNIT + 16 * warp;
+            if (j0 < ahead.len) {
+                const bool ok = page >= 0 && page < c.num_pages;
+                if (!ok && lane == 0) set_dev_error(DEVERR_BAD_PAGE);
+                const size_t row0 = cache_row<D>(c, ok ? page : 0, ahead.g, j0);
+                const uint32_t st = ring + (uint32_t)(i % ST) * STAGEB;
+#pragma unroll
+                for (int q = 0; q < 2 * 16 * NCH / 32; ++q) {
+                    const int x = q * 32 + lane;
+                    const int which = x / (16 * NCH), rem = x % (16 * NCH), r = rem / NCH, ch = rem % NCH;
+                    const uint16_t *src = (which ? c.v : c.k) + row0 + (size_t)r * D + 8 * ch;
+                    // rows past the last token hold anything: they come in as zeros
+                    cp_async16_or_zero(st + which * TILEB + r * ROWB + ((ch ^ (r & 7)) << 4), src,
+                                       ok && j0 + r < ahead.len);
+                }
+            }
+            next_unit(c, ahead);
+            page = lookup(ahead);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) issue(i);
+
+    float(*sm_m)[8 * NG] = reinterpret_cast<float(*)[8 * NG]>(dsm + SM::RING);
+    float(*sm_l)[8 * NG] = sm_m + PD_WARPS;
+    float(*sm_o)[8 * NG][D] = reinterpret_cast<float(*)[8 * NG][D]>(dsm + SM::RING + 2 * PD_WARPS * 8 * NG * 4);
+
+    uint32_t qa[D / 16][2 * NG];
+    float o[NG][D / 8][4], m[NG], l[NG];
+    bool fresh = true;
+    int pair = 0;   // pairs of this run so far
+    for (int i = 0; i < steps; ++i) {
+        if (fresh) {
+            // Q as the A operand: MMA row r is query head r of the kv head (rows >= G are zero)
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+                const int h = 8 * gg + gr;
+                const uint16_t *qr = a.q + ((size_t)cur.b * a.H + (size_t)cur.g * G + (h < G ? h : 0)) * D;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t x0 = __ldg(reinterpret_cast<const unsigned int *>(qr + 16 * ks + 2 * t));
+                    const uint32_t x1 = __ldg(reinterpret_cast<const unsigned int *>(qr + 16 * ks + 8 + 2 * t));
+                    qa[ks][2 * gg] = h < G ? x0 : 0u;
+                    qa[ks][2 * gg + 1] = h < G ? x1 : 0u;
+                }
+                m[gg] = -INFINITY;
+                l[gg] = 0.f;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[gg][n][e] = 0.f;
+            }
+            fresh = false;
+        }
+        issue(i + ST - 1);
+        cp_async_wait<ST - 1>();
+        __syncwarp();   // every lane's copies of step i are in and visible to the warp
+        const uint32_t st = ring + (uint32_t)(i % ST) * STAGEB;
+        const int j0 = cur.u * PD_UNIT + 16 * warp;
+        if (j0 < cur.len) {
+            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            {
+                const int key = (lane & 7) + ((lane >> 4) << 3), hcol = (lane >> 3) & 1;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    uint32_t r[4];
+                    ldsm_x4(st + key * ROWB + (((2 * ks + hcol) ^ (key & 7)) << 4), r);
+                    const uint32_t aq[4] = {qa[ks][0], NG == 2 ? qa[ks][2 * NG - 2] : 0u, qa[ks][1],
+                                            NG == 2 ? qa[ks][2 * NG - 1] : 0u};
+                    if constexpr (XT == X_F16) {
+                        mma_f16_16816(sc[0], aq, r[0], r[1], sc[0]);
+                        mma_f16_16816(sc[1], aq, r[2], r[3], sc[1]);
+                    } else {
+                        mma_bf16_16816(sc[0], aq, r[0], r[1], sc[0]);
+                        mma_bf16_16816(sc[1], aq, r[2], r[3], sc[1]);
+                    }
+                }
+            }
+            uint32_t ap[NG][4], ap3[NG][4];
+            float corr[NG];
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+                // head 8 gg + gr's scores of keys 2t, 2t + 1, 8 + 2t, 9 + 2t, in the log2 domain
+                float p[4] = {sc[0][2 * gg], sc[0][2 * gg + 1], sc[1][2 * gg], sc[1][2 * gg + 1]};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = 8 * (e >> 1) + 2 * t + (e & 1);
+                    p[e] = j0 + key < cur.len ? p[e] * a.qscale : -INFINITY;
+                }
+                float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = fmaxf(m[gg], mx);      // finite: key j0 is live
+                corr[gg] = exp2f(m[gg] - mn);           // 0 on the first step (m = -inf)
+                float ps = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = exp2f(p[e] - mn);            // 0 for a key past the end
+                    ps += p[e];
+                }
+                l[gg] = fmaf(l[gg], corr[gg], ps);
+                m[gg] = mn;
+                const uint32_t h0 = pack16<XT>(p[0], p[1]), h1 = pack16<XT>(p[2], p[3]);
+                const float r0 = p[0] - lo16<XT>(h0), r1 = p[1] - hi16<XT>(h0);
+                const float r2 = p[2] - lo16<XT>(h1), r3 = p[3] - hi16<XT>(h1);
+                const uint32_t l0 = pack16<XT>(r0, r1), l1 = pack16<XT>(r2, r3);
+                ap[gg][0] = h0;
+                ap[gg][1] = l0;
+                ap[gg][2] = h1;
+                ap[gg][3] = l1;
+                if constexpr (PARTS == 3) {
+                    ap3[gg][0] = pack16<XT>(r0 - lo16<XT>(l0), r1 - hi16<XT>(l0));
+                    ap3[gg][1] = 0u;
+                    ap3[gg][2] = pack16<XT>(r2 - lo16<XT>(l1), r3 - hi16<XT>(l1));
+                    ap3[gg][3] = 0u;
+                }
+            }
+            const int key = (lane & 7) + (((lane >> 3) & 1) << 3), hcol = lane >> 4;
+#pragma unroll
+            for (int p2 = 0; p2 < D / 16; ++p2) {
+                uint32_t r[4];
+                ldsm_x4_t(st + TILEB + key * ROWB + (((2 * p2 + hcol) ^ (key & 7)) << 4), r);
+#pragma unroll
+                for (int gg = 0; gg < NG; ++gg) {
+                    // the products of these 16 keys alone: the tensor cores truncate what they add up, which over
+                    // many steps would pull every sum towards zero (1.2e-6 of the result after 64 steps, against
+                    // 3e-7 this way), so the running sum is kept here, rescaled and added in one rounded FMA
+                    float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+                    if constexpr (XT == X_F16) {
+                        mma_f16_16816(x0, ap[gg], r[0], r[1], x0);
+                        mma_f16_16816(x1, ap[gg], r[2], r[3], x1);
+                    } else {
+                        if constexpr (PARTS == 3) {
+                            mma_bf16_16816(x0, ap3[gg], r[0], r[1], x0);
+                            mma_bf16_16816(x1, ap3[gg], r[2], r[3], x1);
+                        }
+                        mma_bf16_16816(x0, ap[gg], r[0], r[1], x0);
+                        mma_bf16_16816(x1, ap[gg], r[2], r[3], x1);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[gg][2 * p2][e] = fmaf(o[gg][2 * p2][e], corr[gg], x0[e]);
+                        o[gg][2 * p2 + 1][e] = fmaf(o[gg][2 * p2 + 1][e], corr[gg], x1[e]);
+                    }
+                }
+            }
+        }
+        __syncwarp();   // the stage is read before a later step's copies refill it
+
+        const bool end_of_pair = cur.u + 1 == cur.n, last = i + 1 == steps;
+        if (end_of_pair || last) {
+            // merge the warps: per head the largest running maximum, the others rescaled to it
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+                const int h = 8 * gg + gr;
+                float ls = l[gg];
+                ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+                ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+                if (t == 0) {
+                    sm_m[warp][h] = m[gg];
+                    sm_l[warp][h] = ls;
+                }
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {   // hi rows + lo rows
+                    sm_o[warp][h][8 * n + 2 * t] = o[gg][n][0] + o[gg][n][2];
+                    sm_o[warp][h][8 * n + 2 * t + 1] = o[gg][n][1] + o[gg][n][3];
+                }
+            }
+            __syncthreads();
+            // a pair that this run began and finished is complete; any other is a part of one
+            const bool complete = end_of_pair && (pair > 0 || i + 1 >= cur.n);
+            for (int x = threadIdx.x; x < G * D; x += PD_WARPS * 32) {
+                const int h = x / D, e = x % D;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < PD_WARPS; ++w) M = fmaxf(M, sm_m[w][h]);
+                float L = 0.f, A = 0.f;   // M is finite: the first warp's first key is live
+#pragma unroll
+                for (int w = 0; w < PD_WARPS; ++w) {
+                    const float f = exp2f(sm_m[w][h] - M);
+                    L = fmaf(sm_l[w][h], f, L);
+                    A = fmaf(sm_o[w][h][e], f, A);
+                }
+                const size_t bh = (size_t)cur.b * a.H + (size_t)cur.g * G + h;
+                if (complete && !d.whole) {
+                    if (a.out16)
+                        static_cast<uint16_t *>(a.out)[bh * D + e] = (uint16_t)pack16<XT>(A / L, 0.f);
+                    else
+                        static_cast<float *>(a.out)[bh * D + e] = A / L;
+                } else {
+                    float *pp = complete ? d.whole + bh * part_stride(D)
+                                         : d.slots + (((size_t)blockIdx.x * 2 + (pair > 0)) * G + h) * part_stride(D);
+                    if (e == 0) {
+                        pp[0] = M;
+                        pp[1] = L;
+                    }
+                    pp[4 + e] = A;
+                }
+            }
+            __syncthreads();   // the merge space is free again
+            ++pair;
+            fresh = true;
+        }
+        next_unit(c, cur);
+    }
+    pdl_launch_dependents();
+}
+
+// Merges partial results: one block per (sequence, query head), D columns by
+// blockDim.x / D groups of threads, each group taking every so-manieth partial.
+// The partials of a pair are, in this order: the prefix's splits, then the
+// pair's own -- the slots of the CTAs whose runs it spans, or the result of the
+// one CTA that finished it.  The order of every addition is fixed by the sizes.
+struct PagedCombineArgs {
+    PagedDecodeArgs d;
+    const float *prefix;     // [(row / 256 * Hkv + g) * splits + s][256] rows, row = b G + h; or null
+    int splits;
+};
+constexpr int PC_THREADS = 512;
+
+template <int XT, int D>
+__global__ void __launch_bounds__(PC_THREADS) paged_combine_kernel(const PagedCombineArgs k) {
+    constexpr int NGR = PC_THREADS / D, PS = part_stride(D);
+    __shared__ float gm[NGR], gl[NGR], go[NGR][D];
+    const PagedAttnArgs &a = k.d.a;
+    const PagedArgs &c = a.c;
+    const int b = blockIdx.x / a.H, hh = blockIdx.x % a.H, g = hh / a.G, h = hh % a.G;
+    long before, all;
+    units_before(c, b, &before, &all);
+    const int n = units_of(own_len(c, b));
+    pdl_wait();
+    // the CTAs whose runs meet this pair's units [first, first + n)
+    int i0 = 0, own = 0;
+    bool whole = false, inner = false;
+    if (n > 0) {
+        const long total = all * c.Hkv, first = before * c.Hkv + (long)g * n;
+        const Runs runs(total, k.d.ctas);
+        i0 = runs.cta_of(first);
+        own = runs.cta_of(first + n - 1) - i0 + 1;
+        whole = own == 1;
+        inner = runs.start(i0) < first;   // the first CTA began in an earlier pair
+        if (whole && !k.prefix) return;                    // written already
+    }
+    const int count = (k.prefix ? k.splits : 0) + own;
+    const int pre = count - own;
+    const int e = threadIdx.x % D, grp = threadIdx.x / D;
+    const size_t row = (size_t)b * a.G + h;
+    auto slot = [&](int i) -> const float * {
+        if (i < pre) return k.prefix + ((((row >> 8) * c.Hkv + g) * k.splits + i) * 256 + (row & 255)) * PS;
+        i -= pre;
+        if (whole) return k.d.whole + ((size_t)b * a.H + hh) * PS;
+        return k.d.slots + (((size_t)(i0 + i) * 2 + (i == 0 && inner)) * a.G + h) * PS;
+    };
+    float M = -INFINITY, L = 0.f, A = 0.f;
+    constexpr int U = 4;
+    for (int s0 = grp; s0 < count; s0 += NGR * U) {
+        float mv[U], lv[U], av[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * NGR;
+            mv[u] = -INFINITY;
+            if (s < count) {
+                const float *p = slot(s);
+                mv[u] = __ldcg(p);
+                lv[u] = __ldcg(p + 1);
+                av[u] = __ldcg(p + 4 + e);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (mv[u] == -INFINITY) continue;
+            const float mn = fmaxf(M, mv[u]), fo = exp2f(M - mn), fn = exp2f(mv[u] - mn);
+            L = fmaf(L, fo, lv[u] * fn);
+            A = fmaf(A, fo, av[u] * fn);
+            M = mn;
+        }
+    }
+    if (e == 0) {
+        gm[grp] = M;
+        gl[grp] = L;
+    }
+    go[grp][e] = A;
+    __syncthreads();
+    if (grp) return;
+    float Mt = -INFINITY, Lt = 0.f, At = 0.f;
+#pragma unroll
+    for (int i = 0; i < NGR; ++i) Mt = fmaxf(Mt, gm[i]);
+#pragma unroll
+    for (int i = 0; i < NGR; ++i) {
+        if (gm[i] == -INFINITY) continue;
+        const float f = exp2f(gm[i] - Mt);
+        Lt = fmaf(gl[i], f, Lt);
+        At = fmaf(go[i][e], f, At);
+    }
+    const float r = Lt > 0.f ? At / Lt : 0.f;   // no token at all: zeros
+    const size_t at = ((size_t)b * a.H + hh) * D + e;
+    if (a.out16)
+        static_cast<uint16_t *>(a.out)[at] = (uint16_t)pack16<XT>(r, 0.f);
+    else
+        static_cast<float *>(a.out)[at] = r;
+}
+
+}  // namespace lwq
