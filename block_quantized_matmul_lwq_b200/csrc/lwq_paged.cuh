@@ -202,66 +202,59 @@ struct PagedAttnArgs {
     float qscale;       // scale * log2(e)
 };
 
-// One warp per (token, query head): the running maximum and sum over the keys
-// that the token sees, one key at a time.
-template <int XT, int D>
-__global__ void __launch_bounds__(128) paged_attn_rows_kernel(const PagedAttnArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long w = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int t = (int)(w / a.H), h = (int)(w % a.H), g = h / a.G;
-    if (t >= a.T) return;
-    const PagedArgs &c = a.c;
-    int b = t, idx = 0, n = 1;
-    if (a.cu) {
-        int cnt = 0;
-        for (int i = lane; i < c.B; i += 32) cnt += __ldg(a.cu + i + 1) <= t;
-        b = __reduce_add_sync(0xffffffffu, cnt);
-        if (b >= c.B) return;
-        const int t0 = __ldg(a.cu + b);
-        idx = t - t0;
-        n = __ldg(a.cu + b + 1) - t0;
-        if (idx < 0 || idx >= n) return;
-    }
-    const long cap = (long)c.max_pages * c.page;
-    const long place = (long)__ldg(c.lens + b) - n + idx;
-    const int own = (int)(place + 1 < 0 ? 0 : place + 1 > cap ? cap : place + 1);
-    const int pre = place < 0 && a.causal ? 0 : c.prefix_len;
-    float qf[E], acc[E], m = -INFINITY, l = 0.f;
-    load_row<XT, E>(a.q + ((size_t)t * a.H + h) * D + E * lane, qf);
+// floats of one partial result: m (log2 domain), l, two unused, acc[D]
+__host__ __device__ constexpr int part_stride(int D) { return D + 4; }
+
+// A list of `count` runs laid end to end, their lengths given by weight(i):
+// all NT threads of a block build it together (each sums a stretch of runs) and
+// then find the run that holds a place.  scratch: NT / 32 + 2 words of shared
+// memory, free for other use after a barrier behind the last call.
+template <int NT>
+struct RunScan {
+    int lo, hi;
+    long excl, mine, all;
+    template <class W>
+    __device__ __forceinline__ RunScan(int count, long *scratch, W weight) {
+        const int per = (count + NT - 1) / NT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        lo = min(count, (int)threadIdx.x * per);
+        hi = min(count, lo + per);
+        mine = 0;
+        for (int i = lo; i < hi; ++i) mine += weight(i);
+        long incl = mine;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int j = 0; j < pre + own; ++j) {
-        const int jj = j < pre ? j : j - pre;
-        const int p = page_of(c, j < pre ? c.prefix : c.tables + (size_t)b * c.max_pages, jj);
-        float kf[E], vf[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) kf[e] = vf[e] = 0.f;
-        if (p >= 0) {
-            load_row<XT, E>(c.k + cache_row<D>(c, p, g, jj) + E * lane, kf);
-            load_row<XT, E>(c.v + cache_row<D>(c, p, g, jj) + E * lane, vf);
+        for (int o = 1; o < 32; o <<= 1) {
+            const long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
         }
-        float s = 0.f;
+        if (lane == 31) scratch[warp] = incl;
+        __syncthreads();
+        all = 0;
+        excl = incl - mine;
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(qf[e], kf[e], s);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= a.qscale;
-        const float mn = fmaxf(m, s), f = exp2f(m - mn), pr = exp2f(s - mn);
-        m = mn;
-        l = fmaf(l, f, pr);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], f, pr * vf[e]);
+        for (int i = 0; i < NT / 32; ++i) {
+            if (i < warp) excl += scratch[i];
+            all += scratch[i];
+        }
     }
-    const float r = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const size_t at = ((size_t)t * a.H + h) * D + E * lane + e;
-        if (a.out16)
-            static_cast<uint16_t *>(a.out)[at] = (uint16_t)pack16<XT>(acc[e] * r, 0.f);
-        else
-            static_cast<float *>(a.out)[at] = acc[e] * r;
+    // The run that holds place `want` < all, and the sum of those before it.
+    template <class W>
+    __device__ __forceinline__ void locate(long want, long *scratch, int *run, long *before, W weight) const {
+        if (want >= excl && want < excl + mine) {
+            long at = excl;
+            for (int i = lo; i < hi; ++i) {
+                const long n = weight(i);
+                if (want < at + n) {
+                    scratch[NT / 32] = i;
+                    scratch[NT / 32 + 1] = at;
+                    break;
+                }
+                at += n;
+            }
+        }
+        __syncthreads();
+        *run = (int)scratch[NT / 32];
+        *before = scratch[NT / 32 + 1];
     }
-}
+};
 
 }  // namespace lwq

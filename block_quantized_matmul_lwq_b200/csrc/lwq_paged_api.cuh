@@ -11,6 +11,7 @@
 #include "../../include/lwq.h"
 #include "lwq_paged.cuh"
 #include "lwq_paged_decode.cuh"
+#include "lwq_paged_tile.cuh"
 
 namespace lwq {
 namespace {
@@ -123,17 +124,6 @@ int paged_workspace(int dev, size_t need, void **ws) {
     return LWQ_OK;
 }
 
-cudaError_t launch_rows(int dtype, int D, const PagedAttnArgs &a, cudaStream_t st) {
-    const unsigned blocks = (unsigned)(((long)a.T * a.H + 3) / 4);
-    if (dtype == LWQ_ACT_F16)
-        D == 64 ? paged_attn_rows_kernel<X_F16, 64><<<blocks, 128, 0, st>>>(a)
-                : paged_attn_rows_kernel<X_F16, 128><<<blocks, 128, 0, st>>>(a);
-    else
-        D == 64 ? paged_attn_rows_kernel<X_BF16, 64><<<blocks, 128, 0, st>>>(a)
-                : paged_attn_rows_kernel<X_BF16, 128><<<blocks, 128, 0, st>>>(a);
-    return cudaGetLastError();
-}
-
 // ------------------------------------------------------------------ decode
 constexpr int kDecodeCtasPerSm = 2;
 
@@ -155,6 +145,101 @@ template <int D>
 cudaError_t launch_paged_decode_x(int dtype, const PagedDecodeArgs &d, const PagedCombineArgs &k, cudaStream_t st) {
     if (dtype == LWQ_ACT_F16) return launch_paged_decode_g<X_F16, D, 2>(d, k, st);
     return d.a.out16 ? launch_paged_decode_g<X_BF16, D, 2>(d, k, st) : launch_paged_decode_g<X_BF16, D, 3>(d, k, st);
+}
+
+// -------------------------------------------------------------- row tiles
+template <int XT, int D, int PARTS>
+int launch_paged_tile(const lwq_paged *c, PagedTileArgs &t, long pairs, cudaStream_t st) {
+    // three parts of a probability fit beside each other for 64 keys at a time
+    constexpr int KT = PARTS == 3 ? 64 : 128;
+    auto kern = paged_tile_kernel<XT, D, PARTS, KT>;
+    constexpr size_t smem = TileSmem<D, KT>::TOTAL;
+    const int brows = c->page < KT ? c->page : KT;
+    CUtensorMap maps[2];
+    for (int i = 0; i < 2; ++i) {
+        MapReq r = map_req(i ? c->v : c->k, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, CU_TENSOR_MAP_SWIZZLE_128B);
+        r.dims[0] = (cuuint64_t)D;
+        r.dims[1] = (cuuint64_t)t.total_rows;
+        r.strides[0] = (cuuint64_t)D * 2;
+        r.box[0] = 64;
+        r.box[1] = (cuuint32_t)brows;
+        if (encode_cached(r, &maps[i])) return LWQ_ERR_CUDA;
+    }
+    if (ensure_smem(reinterpret_cast<const void *>(kern), smem) != cudaSuccess) return LWQ_ERR_CUDA;
+    if (launch_k(kern, (int)(pairs * c->Hkv * t.splits), TILE_THREADS, smem, st, false, maps[0], maps[1], t) != cudaSuccess)
+        return LWQ_ERR_CUDA;
+    if (t.prefix_only || t.splits == 1) return LWQ_OK;
+    return launch_k(paged_tile_combine_kernel<XT, D>, (int)(pairs * c->Hkv * (PAIR_ROWS / 8)), 256, 0, st, true, t) ==
+                   cudaSuccess
+               ? LWQ_OK
+               : LWQ_ERR_CUDA;
+}
+// The parts of a probability: see the kernel's header.  A prefix's partial results go on to other sums in fp32, but a
+// 16-bit result is no nearer for that.
+template <int D>
+int launch_paged_tile_x(const lwq_paged *c, PagedTileArgs &t, long pairs, cudaStream_t st) {
+    if (c->dtype == LWQ_ACT_F16)
+        return t.a.out16 ? launch_paged_tile<X_F16, D, 1>(c, t, pairs, st) : launch_paged_tile<X_F16, D, 2>(c, t, pairs, st);
+    return t.a.out16 ? launch_paged_tile<X_BF16, D, 1>(c, t, pairs, st) : launch_paged_tile<X_BF16, D, 3>(c, t, pairs, st);
+}
+
+PagedTileArgs paged_tile_args(const lwq_paged *c, const PagedAttnArgs &a, int splits, float *part) {
+    PagedTileArgs t;
+    t.a = a;
+    t.flip = a.qscale < 0.f;
+    t.a.qscale = fabsf(a.qscale);
+    if (t.a.qscale < 1e-30f) t.a.qscale = 1e-30f;   // scale 0: a masked score stays -inf, any other becomes 0
+    t.part = part;
+    t.splits = splits;
+    t.prefix_only = 0;
+    t.total_rows = c->num_pages * c->Hkv * c->page;
+    t.timeout_ns = kTimeoutNs;
+    return t;
+}
+
+// Pairs of row tiles that T tokens of at most B sequences can make, and into how many parts each pair's keys are cut:
+// one when the pairs fill the GPU (a CTA per SM), else as many as do, but no part below one tile of 128 keys.
+long tile_pairs(long T, int B, int G) { return T * G / PAIR_ROWS + (B < T ? B : T); }
+int tile_splits(long pairs, int Hkv, long keys, int sms) {
+    const long items = pairs * Hkv;
+    long s = items >= sms ? 1 : sms / items;
+    const long tiles = (keys + 127) / 128;
+    if (s > tiles) s = tiles;
+    return s < 1 ? 1 : (int)s;
+}
+size_t tile_part_bytes(long pairs, int Hkv, int splits, int D) {
+    return (size_t)pairs * Hkv * splits * PAIR_ROWS * part_stride(D) * sizeof(float);
+}
+
+// How a prefill call is divided.
+void prefill_plan(const lwq_paged *c, int T, int H, int sms, long *pairs, int *splits) {
+    *pairs = tile_pairs(T, c->B, H / c->Hkv);
+    *splits = tile_splits(*pairs, c->Hkv, (long)c->max_pages * c->page + c->prefix_len, sms);
+}
+
+// The parts of a decode call's workspace: the CTAs' slots, then, with a prefix, one result per (sequence, head) and
+// the prefix's partial results.
+struct DecodeSpace {
+    size_t slots, whole, prefix;
+    long pairs;
+    int splits;
+    size_t total() const { return slots + whole + prefix; }
+};
+DecodeSpace decode_space(const lwq_paged *c, int H, int sms) {
+    DecodeSpace s;
+    const int G = H / c->Hkv;
+    const size_t ps = part_stride(c->D) * sizeof(float);
+    s.slots = (size_t)kDecodeCtasPerSm * sms * 2 * G * ps;
+    s.whole = s.prefix = 0;
+    s.pairs = 0;
+    s.splits = 0;
+    if (c->prefix_len > 0) {
+        s.whole = (size_t)c->B * H * ps;
+        s.pairs = pairs_of(c->B, G);
+        s.splits = tile_splits(s.pairs, c->Hkv, c->prefix_len, sms);
+        s.prefix = tile_part_bytes(s.pairs, c->Hkv, s.splits, c->D);
+    }
+    return s;
 }
 
 }  // namespace
@@ -264,8 +349,7 @@ size_t lwq_attention_paged_workspace_size(const lwq_paged *cache, int H) {
     if (paged_sizes(cache, H)) return 0;
     int dev = 0, sms = 148;
     if (current_device(&dev) == LWQ_OK) sms = sm_count(dev);
-    const size_t ps = part_stride(cache->D) * sizeof(float);
-    return (size_t)kDecodeCtasPerSm * sms * 2 * (H / cache->Hkv) * ps;
+    return decode_space(cache, H, sms).total();
 }
 
 int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *out, int H, float scale,
@@ -276,14 +360,10 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
     if (rc) return rc;
     int dev;
     if ((rc = current_device(&dev))) return rc;
+    const DecodeSpace sp = decode_space(cache, H, sm_count(dev));
     void *ws;
-    if ((rc = paged_workspace(dev, lwq_attention_paged_workspace_size(cache, H), &ws))) return rc;
+    if ((rc = paged_workspace(dev, sp.total(), &ws))) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cache->prefix_len > 0) {
-        if (launch_rows(cache->dtype, cache->D, a, st) != cudaSuccess) return LWQ_ERR_CUDA;
-        t_last_launches = 1;
-        return LWQ_OK;
-    }
     PagedCombineArgs k;
     PagedDecodeArgs &d = k.d;
     d.a = a;
@@ -292,16 +372,35 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
     d.ctas = kDecodeCtasPerSm * sm_count(dev);
     k.prefix = nullptr;
     k.splits = 0;
+    int launches = 2;
+    if (cache->prefix_len > 0) {
+        d.whole = d.slots + sp.slots / sizeof(float);
+        k.splits = sp.splits;
+        float *part = d.whole + sp.whole / sizeof(float);
+        k.prefix = part;
+        PagedTileArgs t = paged_tile_args(cache, a, sp.splits, part);
+        t.prefix_only = 1;
+        if ((rc = cache->D == 64 ? launch_paged_tile_x<64>(cache, t, sp.pairs, st)
+                                 : launch_paged_tile_x<128>(cache, t, sp.pairs, st)))
+            return rc;
+        ++launches;
+    }
     const cudaError_t e = cache->D == 64 ? launch_paged_decode_x<64>(cache->dtype, d, k, st)
                                          : launch_paged_decode_x<128>(cache->dtype, d, k, st);
     if (e != cudaSuccess) return LWQ_ERR_CUDA;
-    t_last_launches = 2;
+    t_last_launches = launches;
     return LWQ_OK;
 }
 
 size_t lwq_attention_prefill_workspace_size(const lwq_paged *cache, int T, int H) {
     if (paged_sizes(cache, H) || T <= 0) return 0;
-    return 256;
+    int dev = 0, sms = 148;
+    if (current_device(&dev) == LWQ_OK) sms = sm_count(dev);
+    long pairs;
+    int splits;
+    prefill_plan(cache, T, H, sms, &pairs, &splits);
+    const size_t need = splits > 1 ? tile_part_bytes(pairs, cache->Hkv, splits, cache->D) : 0;
+    return need < 256 ? 256 : need;
 }
 
 int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void *out, const int32_t *cu_tokens,
@@ -312,9 +411,17 @@ int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void
     if (rc) return rc;
     int dev;
     if ((rc = current_device(&dev))) return rc;
-    if (launch_rows(cache->dtype, cache->D, a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return LWQ_ERR_CUDA;
-    t_last_launches = 1;
+    long pairs;
+    int splits;
+    prefill_plan(cache, T, H, sm_count(dev), &pairs, &splits);
+    if ((double)pairs * cache->Hkv * splits * (PAIR_ROWS / 8) > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
+    void *ws;
+    if ((rc = paged_workspace(dev, splits > 1 ? tile_part_bytes(pairs, cache->Hkv, splits, cache->D) : 0, &ws))) return rc;
+    PagedTileArgs t = paged_tile_args(cache, a, splits, static_cast<float *>(ws));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if ((rc = cache->D == 64 ? launch_paged_tile_x<64>(cache, t, pairs, st) : launch_paged_tile_x<128>(cache, t, pairs, st)))
+        return rc;
+    t_last_launches = splits > 1 ? 2 : 1;
     return LWQ_OK;
 }
 

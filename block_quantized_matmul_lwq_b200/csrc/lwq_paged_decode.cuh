@@ -25,9 +25,6 @@ namespace lwq {
 constexpr int PD_WARPS = 4;
 constexpr int PD_UNIT = 64;     // keys of a unit: 16 per warp
 
-// floats of one partial result: m (log2 domain), l, two unused, acc[D]
-__host__ __device__ constexpr int part_stride(int D) { return D + 4; }
-
 // 16 bytes from global to shared, or zeros (the source is not read then)
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool live) {
     const int n = live ? 16 : 0;
@@ -124,60 +121,26 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
     constexpr uint32_t ROWB = SM::ROWB, TILEB = SM::TILEB, STAGEB = SM::STAGEB;
     extern __shared__ __align__(128) uint8_t dsm[];
     // the scan's words, in the dynamic space (its limit is raised to all that a block may have)
-    long *const s_warp = reinterpret_cast<long *>(dsm + SM::RING + SM::MERGE);
-    long *const s_before = s_warp + PD_WARPS;
-    int *const s_b = reinterpret_cast<int *>(s_before + 1);
+    long *const scratch = reinterpret_cast<long *>(dsm + SM::RING + SM::MERGE);
     const PagedAttnArgs &a = d.a;
     const PagedArgs &c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3, G = a.G;
 
-    // this CTA's run of units, and the sequence that it begins in: a scan of the lengths, each
-    // thread taking a run of sequences
-    const int per = (c.B + PD_WARPS * 32 - 1) / (PD_WARPS * 32);
-    const int b_lo = min(c.B, (int)threadIdx.x * per), b_hi = min(c.B, b_lo + per);
-    long mine = 0;
-    for (int i = b_lo; i < b_hi; ++i) mine += units_of(own_len(c, i));
-    long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    long all = 0, excl = incl - mine;
-#pragma unroll
-    for (int i = 0; i < PD_WARPS; ++i) {
-        if (i < warp) excl += s_warp[i];
-        all += s_warp[i];
-    }
-    const long total = all * c.Hkv;
+    // this CTA's run of units, and the sequence that it begins in
+    auto units = [&](int b) { return units_of(own_len(c, b)); };
+    RunScan<PD_WARPS * 32> scan(c.B, scratch, units);
+    const long total = scan.all * c.Hkv;
     const Runs runs(total, d.ctas);
     const long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
     if (u0 >= u1) return;
-    {
-        const long want = u0 / c.Hkv;   // unit per kv head: before(b) <= want < before(b + 1)
-        if (want >= excl && want < excl + mine) {
-            long at = excl;
-            for (int i = b_lo; i < b_hi; ++i) {
-                const int n = units_of(own_len(c, i));
-                if (want < at + n) {
-                    *s_b = i;
-                    *s_before = at;
-                    break;
-                }
-                at += n;
-            }
-        }
-    }
-    __syncthreads();
-    const int steps = (int)(u1 - u0);
     UnitPos cur;
-    cur.b = *s_b;
+    long before;
+    scan.locate(u0 / c.Hkv, scratch, &cur.b, &before, units);
+    const int steps = (int)(u1 - u0);
     cur.len = own_len(c, cur.b);
     cur.n = units_of(cur.len);
     {
-        const long rem = u0 - *s_before * c.Hkv;
+        const long rem = u0 - before * c.Hkv;
         cur.g = (int)(rem / cur.n);
         cur.u = (int)(rem % cur.n);
     }

@@ -1,0 +1,564 @@
+// Attention of many query rows over one run of keys, on the tcgen05 tensor
+// cores: the prefill of a sequence's new tokens (causal), and a shared prefix
+// against the queries of a whole batch.
+//
+// Rows are (token, query head) pairs of one kv head, row = token * G + head, so
+// that every G fills the 128 rows of an MMA and a key tile is read once for all
+// the heads that share it.  A CTA takes 256 rows (two MMA tiles) of one
+// sequence and kv head, and a contiguous part of the key tiles (all of them
+// when there are enough rows to fill the GPU; partial results are merged by a
+// second kernel otherwise):
+//
+//   warp 0      TMA: key and value tiles through one ring, K0 V0 K1 V1 ...;
+//               a tile is as many boxes as pages it spans
+//   warp 1      tcgen05.mma: S_t = Q_t K^T (both from shared memory), then
+//               O_t += P_t V with P_t in TMEM, over S_t's columns
+//   warps 2, 3  idle (registers are split by groups of four warps)
+//   warps 4..11 softmax, one thread per row: S_t from TMEM, running maximum
+//               and sum in fp32, P_t back to TMEM
+//
+// The two row tiles alternate: while one's scores are in the softmax warps the
+// tensor core works on the other.  A row's output is rescaled only when its
+// running maximum has grown by more than 8 (log2 domain) over the one in use:
+// until then its probabilities may exceed 1, up to 256, which changes nothing
+// but their scale, in numerator and denominator alike.
+//
+// The probabilities are PARTS 16-bit numbers each.  A 16-bit result takes one
+// part (off by half a step of that type per key, like the result's own
+// rounding); an fp32 result takes two in fp16 (22 bits), three in bf16 (24).
+#pragma once
+
+#include "lwq_paged.cuh"
+
+namespace lwq {
+
+constexpr int TILE_ROWS = 128;
+constexpr int PAIR_ROWS = 2 * TILE_ROWS;
+constexpr int TILE_THREADS = 384;
+// registers per thread after the split: 128 x 72 + 256 x 208 = 62464 of the 384 x 168 = 64512 at launch
+constexpr int TILE_REGS_FEED = 72, TILE_REGS_SOFTMAX = 208;
+constexpr uint32_t TILE_TMEM_COLS = 512;
+constexpr float TILE_SLACK = 8.f;      // growth of a row's maximum that needs no rescaling
+
+struct PagedTileArgs {
+    PagedAttnArgs a;
+    float *part;        // partial results [(pair * Hkv + g) * splits + s][256 rows], or null: write out
+    int splits;
+    int prefix_only;    // the batch's queries (one row set of all T tokens) against the prefix alone
+    int flip;           // negative scale: Q's signs are flipped and qscale is positive
+    int total_rows;     // cache rows (num_pages Hkv page): the coordinate of a page that is not there
+    unsigned long long timeout_ns;
+};
+
+// pairs of row tiles of a sequence with n new tokens
+__host__ __device__ __forceinline__ long pairs_of(long n, int G) { return n <= 0 ? 0 : (n * G + PAIR_ROWS - 1) / PAIR_ROWS; }
+
+// The rows of one pair: its sequence, first row, and what its rows see.
+struct RowSet {
+    int b, tok0, n;     // sequence, its first token's row of q, its tokens
+    int row0;           // first row of the pair among the sequence's n * G
+    int len, cap;
+};
+// tokens seen before and at row r: -1 for a row that sees nothing, else the sequence's own tokens
+__device__ __forceinline__ int own_seen(const RowSet &s, int G, int r) {
+    const long place = (long)s.len - s.n + r / G;
+    return place < 0 ? -1 : (int)(place + 1 < s.cap ? place + 1 : s.cap);
+}
+
+template <int D, int KT>
+struct TileSmem {
+    static constexpr uint32_t HALVES = D / 64;                       // 64-element (128-byte) column groups
+    static constexpr uint32_t HALF_Q = TILE_ROWS * 128, HALF_KV = KT * 128;
+    static constexpr uint32_t QB = HALVES * HALF_Q, SLOT = HALVES * HALF_KV;
+    static constexpr int STAGES = (227 * 1024 - 2 * QB - 2048) / SLOT < 8 ? (227 * 1024 - 2 * QB - 2048) / SLOT : 8;
+    static constexpr size_t BARS = 2 * QB + STAGES * SLOT;           // offset of the barriers
+    static constexpr size_t TOTAL = 1024 + BARS + 256;
+};
+
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Operand whose rows are contiguous along N (values [key][D]): 64-element column groups `lead` bytes apart, 8-key
+// groups 1024 bytes apart, 128-byte swizzle.
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint32_t lead) {
+    return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A warpgroup's registers per thread (all of its warps take part).
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int XT, int D, int PARTS, int KT>
+__global__ void __launch_bounds__(TILE_THREADS, 1)
+    paged_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const PagedTileArgs ta) {
+    using SM = TileSmem<D, KT>;
+    static_assert(PARTS * KT / 2 <= 128 && KT <= 128 && KT % 64 == 0, "a tile's scores and probabilities share 128 columns");
+    static_assert(SM::STAGES >= 3, "K and V of a tile and the next K");
+    constexpr int ST = SM::STAGES;
+    constexpr uint32_t IDESC_S = umma_idesc_f16(XT == X_F16 ? 0 : 1, TILE_ROWS, KT);
+    constexpr uint32_t IDESC_O = umma_idesc_f16(XT == X_F16 ? 0 : 1, TILE_ROWS, D) | (1u << 16);   // B along N
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const PagedAttnArgs &a = ta.a;
+    const PagedArgs &c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + SM::BARS);
+    uint64_t *full = bars, *empty = bars + ST, *q_full = bars + 2 * ST, *s_full = q_full + 2, *p_full = s_full + 2,
+             *o_full = p_full + 2, *all_done = o_full + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(all_done + 1);
+
+    // ---- which rows, which kv head, which part of the keys
+    const int group = c.Hkv * ta.splits;
+    const int g = (int)(blockIdx.x % group) / ta.splits, split = (int)(blockIdx.x % ta.splits);
+    const long pair = blockIdx.x / group;
+    RowSet rs;
+    rs.cap = c.max_pages * c.page;
+    long pl;
+    if (ta.prefix_only) {
+        rs.b = 0;
+        rs.tok0 = 0;
+        rs.n = a.T;
+        rs.len = 0;
+        pl = pair;
+    } else {
+        long *scratch = reinterpret_cast<long *>(sm);
+        auto tokens = [&](int b) {
+            if (!a.cu) return 1;
+            const int lo = min(max(__ldg(a.cu + b), 0), a.T), hi = min(__ldg(a.cu + b + 1), a.T);
+            return max(hi - lo, 0);
+        };
+        RunScan<TILE_THREADS> scan(c.B, scratch, [&](int b) { return pairs_of(tokens(b), a.G); });
+        if (pair >= scan.all) return;
+        long before;
+        scan.locate(pair, scratch, &rs.b, &before, [&](int b) { return pairs_of(tokens(b), a.G); });
+        rs.tok0 = a.cu ? min(max(__ldg(a.cu + rs.b), 0), a.T) : rs.b;
+        rs.n = tokens(rs.b);
+        rs.len = __ldg(c.lens + rs.b);
+        pl = pairs_of(rs.n, a.G) - 1 - (pair - before);   // the rows that see most first
+        __syncthreads();                                   // the scratch is shared memory of the tiles
+    }
+    rs.row0 = (int)(pl * PAIR_ROWS);
+    const int rows = min(rs.n * a.G - rs.row0, PAIR_ROWS);   // live rows of the pair
+    const int npre = (c.prefix_len + KT - 1) / KT;
+    // key tiles that row tile t sees, and those of the pair; this CTA takes [j0, j1) of the latter
+    auto tiles_seen = [&](int t) {
+        const int live = min(rows - t * TILE_ROWS, TILE_ROWS);
+        if (live <= 0) return 0;
+        if (ta.prefix_only) return npre;
+        const int seen = own_seen(rs, a.G, rs.row0 + t * TILE_ROWS + live - 1);
+        return seen < 0 ? 0 : npre + (seen + KT - 1) / KT;
+    };
+    const int n0 = tiles_seen(0), n1 = tiles_seen(1), nall = max(n0, n1);
+    const int own_load = ta.prefix_only ? 0 : max(0, own_seen(rs, a.G, rs.row0 + rows - 1));
+    const int j0 = (int)((long)nall * split / ta.splits), j1 = (int)((long)nall * (split + 1) / ta.splits);
+    const int cnt0 = min(max(n0 - j0, 0), j1 - j0), cnt1 = min(max(n1 - j0, 0), j1 - j0), cnt = max(cnt0, cnt1);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 4);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&o_full[t], 1);
+        }
+        mbar_init(all_done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, TILE_TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = *tmem_holder;
+    auto s_col = [&](int t) { return tmem + 128u * t; };
+    auto o_col = [&](int t) { return tmem + 256u + 128u * t; };
+    const uint32_t q_smem = smem_u32(sm), ring = q_smem + 2 * SM::QB;
+    // key tile j of the pair: its first key within its segment, and its live keys
+    auto tile_keys = [&](int j, int *key0) {
+        if (j < npre) {
+            *key0 = j * KT;
+            return min(KT, c.prefix_len - j * KT);
+        }
+        *key0 = (j - npre) * KT;
+        return min(KT, own_load - *key0);
+    };
+
+    if (warp == 0) {
+        // -------------------------------------------------------------- TMA
+        regs_dec<TILE_REGS_FEED>();
+        const int brows = min(c.page, KT);
+        const int *table = c.tables + (size_t)rs.b * c.max_pages;
+        bool ok = true;
+        int i = 0;
+        for (int j = j0; ok && j < j0 + cnt; ++j) {
+            int key0;
+            const int valid = tile_keys(j, &key0);
+            const int boxes = (valid + brows - 1) / brows;
+            const int box = lane / (int)SM::HALVES, half = lane % (int)SM::HALVES;
+            int row = 0;
+            if (box < boxes) {
+                const int p = page_of(c, j < npre ? c.prefix : table, key0 + box * brows);
+                row = p < 0 ? ta.total_rows : (p * c.Hkv + g) * c.page + ((key0 + box * brows) & (c.page - 1));
+            }
+            for (int w = 0; w < 2; ++w, ++i) {
+                const int slot = i % ST;
+                if (i >= ST && !(ok = mbar_wait(&empty[slot], (uint32_t)((i / ST - 1) & 1), ta.timeout_ns, DEVERR_ATTN_WAIT)))
+                    break;
+                if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * brows * D * 2));
+                __syncwarp();
+                if (box < boxes)
+                    tma_load_2d(sm + 2 * SM::QB + (size_t)slot * SM::SLOT + half * SM::HALF_KV + (size_t)box * brows * 128,
+                                w ? &vmap : &kmap, &full[slot], half * 64, row);
+            }
+        }
+        // copies still in flight land before the block ends
+        for (int x = max(0, i - ST); x < i; ++x)
+            mbar_wait(&full[x % ST], (uint32_t)((x / ST) & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- MMA
+        regs_dec<TILE_REGS_FEED>();
+        bool ok = true;
+        auto wait_slot = [&](int i) {
+            return mbar_wait(&full[i % ST], (uint32_t)((i / ST) & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
+        };
+        auto scores = [&](int t, int j) {   // S_t = Q_t K_j^T (one lane)
+            const uint32_t qb = q_smem + t * SM::QB, kb = ring + (uint32_t)((2 * j) % ST) * SM::SLOT;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                umma_f16(s_col(t), umma_desc_sw128(qb + (kk / 4) * SM::HALF_Q + (kk % 4) * 32),
+                         umma_desc_sw128(kb + (kk / 4) * SM::HALF_KV + (kk % 4) * 32), IDESC_S, kk ? 1u : 0u);
+            umma_commit(&s_full[t]);
+        };
+        if (cnt > 0) {
+            ok = wait_slot(0);
+            for (int t = 0; ok && t < 2; ++t) {
+                if ((t ? cnt1 : cnt0) == 0) continue;
+                if (!(ok = mbar_wait(&q_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                tc_fence_after();
+                if (lane == 0) scores(t, 0);
+            }
+            if (ok && lane == 0) umma_commit(&empty[0]);
+            for (int j = 0; ok && j < cnt; ++j) {
+                const int iv = 2 * j + 1;
+                if (!(ok = wait_slot(iv))) break;
+                int key0;
+                const int valid = tile_keys(j0 + j, &key0);
+                if (valid < KT) {
+                    // value rows behind the last key hold anything (NaN): zeros, as P is zero there
+                    const uint32_t vb = ring + (uint32_t)(iv % ST) * SM::SLOT;
+                    for (int x = lane; x < (KT - valid) * 8; x += 32)
+#pragma unroll
+                        for (uint32_t h = 0; h < SM::HALVES; ++h)
+                            st_shared_v4(vb + h * SM::HALF_KV + (uint32_t)(valid * 128 + x * 16), 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (j + 1 < cnt && !(ok = wait_slot(iv + 1))) break;
+                for (int t = 0; ok && t < 2; ++t) {
+                    const int mine = t ? cnt1 : cnt0;
+                    if (j >= mine) continue;
+                    if (!(ok = mbar_wait(&p_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t vb = ring + (uint32_t)(iv % ST) * SM::SLOT;
+#pragma unroll
+                        for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+                            for (int kk = 0; kk < KT / 16; ++kk)
+                                umma_f16_ts(o_col(t), s_col(t) + p * (KT / 2) + kk * 8,
+                                            umma_desc_mn_sw128(vb + kk * 2048, SM::HALF_KV), IDESC_O,
+                                            (j > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
+                        if (j + 1 < mine)
+                            scores(t, j + 1);
+                        else
+                            umma_commit(&o_full[t]);
+                    }
+                }
+                if (ok && lane == 0) {
+                    umma_commit(&empty[iv % ST]);
+                    if (j + 1 < cnt) umma_commit(&empty[(iv + 1) % ST]);
+                }
+            }
+        }
+        if (lane == 0) umma_commit(all_done);   // every MMA is over before TMEM is released
+        __syncwarp();
+        mbar_wait(all_done, 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+    } else if (warp < 4) {
+        regs_dec<TILE_REGS_FEED>();
+    } else {
+        // ---------------------------------------------------------- softmax
+        regs_inc<TILE_REGS_SOFTMAX>();
+        const int t = (warp - 4) >> 2, quarter = warp & 3;
+        const int tid = threadIdx.x & 127;          // thread of the tile's 128
+        const int mine = t ? cnt1 : cnt0;
+        // Q into shared memory: consecutive threads take consecutive 16 bytes of a row
+        if (mine > 0) {
+            constexpr int CH = D / 8;
+            const uint32_t qb = q_smem + t * SM::QB;
+#pragma unroll 4
+            for (int x = tid; x < TILE_ROWS * CH; x += TILE_ROWS) {
+                const int r = x / CH, ch = x % CH, rr = t * TILE_ROWS + r;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (rr < rows) {
+                    const int ri = rs.row0 + rr;
+                    v = __ldg(reinterpret_cast<const uint4 *>(
+                        a.q + ((size_t)(rs.tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D + 8 * ch));
+                    if (ta.flip) {
+                        v.x ^= 0x80008000u;
+                        v.y ^= 0x80008000u;
+                        v.z ^= 0x80008000u;
+                        v.w ^= 0x80008000u;
+                    }
+                }
+                st_shared_v4(qb + (ch / 8) * SM::HALF_Q + r * 128 + (((ch % 8) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[t]);
+        }
+        const int r = t * TILE_ROWS + 32 * quarter + lane;   // this thread's row of the pair
+        const bool live = r < rows;
+        int pre = 0, own = 0;                                // keys of each segment that the row sees
+        if (live) {
+            if (ta.prefix_only) {
+                pre = c.prefix_len;
+            } else {
+                own = own_seen(rs, a.G, rs.row0 + r);
+                pre = own < 0 ? 0 : c.prefix_len;
+            }
+        }
+        const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
+        const uint32_t sc = s_col(t) + lane_off, oc = o_col(t) + lane_off;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < mine; ++j) {
+            if (!(ok = mbar_wait(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+            tc_fence_after();
+            uint32_t s[KT];
+#pragma unroll
+            for (int x = 0; x < KT; x += 32) tmem_ld_32x32b_x32(sc + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
+            tmem_wait_ld();
+            int key0;
+            tile_keys(j0 + j, &key0);
+            const int limit = (j0 + j < npre ? pre : own) - key0;   // keys of the tile that the row sees
+            if (limit < KT) {
+#pragma unroll
+                for (int x = 0; x < KT; ++x)
+                    if (x >= limit) s[x] = 0xff800000u;             // -inf
+            }
+            __syncwarp();
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int x = 0; x < KT; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.qscale;
+            // (the first tile with a live key sets m; O is overwritten by the first product)
+            const bool grown = top > m + TILE_SLACK || (m == -INFINITY && top > m);
+            if (__any_sync(0xffffffffu, grown)) {
+                const float mn = grown ? top : m;
+                const float f = grown ? ex2(m - mn) : 1.f;          // 0 while m = -inf
+                m = mn;
+                l *= f;
+                if (j > 0) {
+#pragma unroll
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(oc + x, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                        tmem_st_32x32b_x32(oc + x, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;            // a row that has seen nothing: all zeros
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x0 = 0; x0 < KT; x0 += 32) {
+                uint32_t h[16];
+#pragma unroll
+                for (int x = 0; x < 32; x += 2) {
+                    const float p0 = ex2(fmaf(__uint_as_float(s[x0 + x]), a.qscale, -base));
+                    const float p1 = ex2(fmaf(__uint_as_float(s[x0 + x + 1]), a.qscale, -base));
+                    sum[x & 3] += p0;
+                    sum[(x & 3) + 1] += p1;
+                    h[x / 2] = pack16<XT>(p0, p1);
+                    s[x0 + x] = __float_as_uint(p0 - lo16<XT>(h[x / 2]));
+                    s[x0 + x + 1] = __float_as_uint(p1 - hi16<XT>(h[x / 2]));
+                }
+                tmem_st_32x32b_x16(sc + x0 / 2, h);
+#pragma unroll
+                for (int p = 1; p < PARTS; ++p) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                        const float r0 = __uint_as_float(s[x0 + x]), r1 = __uint_as_float(s[x0 + x + 1]);
+                        h[x / 2] = pack16<XT>(r0, r1);
+                        s[x0 + x] = __float_as_uint(r0 - lo16<XT>(h[x / 2]));
+                        s[x0 + x + 1] = __float_as_uint(r1 - hi16<XT>(h[x / 2]));
+                    }
+                    tmem_st_32x32b_x16(sc + p * (KT / 2) + x0 / 2, h);
+                }
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[t]);
+        }
+        // ---------------------------------------------------------- results
+        if (mine > 0 && ok) ok = mbar_wait(&o_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+        tc_fence_after();
+        if (ok) {
+            float *pp = nullptr;
+            if (ta.part)
+                pp = ta.part + (((size_t)(pair * c.Hkv + g) * ta.splits + split) * PAIR_ROWS + r) * part_stride(D);
+            if (pp && live) *reinterpret_cast<float2 *>(pp) = make_float2(m, l);
+            const int ri = rs.row0 + r;
+            const size_t at = live ? ((size_t)(rs.tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D : 0;
+            const float inv = ta.part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+#pragma unroll
+            for (int x0 = 0; x0 < D; x0 += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                if (mine > 0) {
+                    tmem_ld_32x32b_x32(oc + x0, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] = 0u;
+                }
+                if (!live) continue;
+                float f[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) f[x] = l > 0.f ? __uint_as_float(o[x]) * inv : 0.f;
+                if (!ta.part && a.out16) {
+                    uint16_t *dst = static_cast<uint16_t *>(a.out) + at + x0;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 8)
+                        *reinterpret_cast<uint4 *>(dst + x) =
+                            make_uint4(pack16<XT>(f[x], f[x + 1]), pack16<XT>(f[x + 2], f[x + 3]),
+                                       pack16<XT>(f[x + 4], f[x + 5]), pack16<XT>(f[x + 6], f[x + 7]));
+                } else {
+                    float *dst = ta.part ? pp + 4 + x0 : static_cast<float *>(a.out) + at + x0;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4)
+                        *reinterpret_cast<float4 *>(dst + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
+                }
+            }
+        }
+        tc_fence_before();
+    }
+
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TILE_TMEM_COLS);
+    }
+}
+
+// Merges the key splits of a prefill: a warp per (row, kv head), its lanes the
+// columns; the splits in order, eight loads in flight.
+template <int XT, int D>
+__global__ void __launch_bounds__(256) paged_tile_combine_kernel(const PagedTileArgs ta) {
+    constexpr int PS = part_stride(D), E = D / 32, U = 4;
+    const PagedAttnArgs &a = ta.a;
+    const PagedArgs &c = a.c;
+    __shared__ long scratch[16];
+    const int lane = threadIdx.x & 31;
+    const long item = blockIdx.x / (PAIR_ROWS / 8);       // (pair, kv head)
+    const int r = (int)(blockIdx.x % (PAIR_ROWS / 8)) * 8 + (threadIdx.x >> 5);
+    const int g = (int)(item % c.Hkv);
+    const long pair = item / c.Hkv;
+    auto tokens = [&](int b) {
+        if (!a.cu) return 1;
+        const int lo = min(max(__ldg(a.cu + b), 0), a.T), hi = min(__ldg(a.cu + b + 1), a.T);
+        return max(hi - lo, 0);
+    };
+    RunScan<256> scan(c.B, scratch, [&](int b) { return pairs_of(tokens(b), a.G); });
+    if (pair >= scan.all) return;
+    int b;
+    long before;
+    scan.locate(pair, scratch, &b, &before, [&](int b) { return pairs_of(tokens(b), a.G); });
+    const int n = tokens(b), tok0 = a.cu ? min(max(__ldg(a.cu + b), 0), a.T) : b;
+    const long ri = (pairs_of(n, a.G) - 1 - (pair - before)) * PAIR_ROWS + r;
+    if (ri >= (long)n * a.G) return;
+    pdl_wait();
+    const float *p0 = ta.part + (((size_t)(pair * c.Hkv + g) * ta.splits) * PAIR_ROWS + r) * PS;
+    float M = -INFINITY, L = 0.f, A[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) A[e] = 0.f;
+    for (int s0 = 0; s0 < ta.splits; s0 += U) {
+        float mv[U], lv[U], av[U][E];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mv[u] = -INFINITY;
+            if (s0 + u < ta.splits) {
+                const float *p = p0 + (size_t)(s0 + u) * PAIR_ROWS * PS;
+                mv[u] = __ldcg(p);
+                lv[u] = __ldcg(p + 1);
+#pragma unroll
+                for (int e = 0; e < E; ++e) av[u][e] = __ldcg(p + 4 + 32 * e + lane);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (mv[u] == -INFINITY) continue;
+            const float mn = fmaxf(M, mv[u]), fo = exp2f(M - mn), fn = exp2f(mv[u] - mn);
+            L = fmaf(L, fo, lv[u] * fn);
+#pragma unroll
+            for (int e = 0; e < E; ++e) A[e] = fmaf(A[e], fo, av[u][e] * fn);
+            M = mn;
+        }
+    }
+    const size_t at = ((size_t)(tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const float v = L > 0.f ? A[e] / L : 0.f;
+        if (a.out16)
+            static_cast<uint16_t *>(a.out)[at + 32 * e + lane] = (uint16_t)pack16<XT>(v, 0.f);
+        else
+            static_cast<float *>(a.out)[at + 32 * e + lane] = v;
+    }
+}
+
+}  // namespace lwq
