@@ -35,10 +35,14 @@ namespace lwq {
 constexpr int TILE_ROWS = 128;
 constexpr int PAIR_ROWS = 2 * TILE_ROWS;
 constexpr int TILE_THREADS = 384;
-// registers per thread after the split: 128 x 72 + 256 x 208 = 62464 of the 384 x 168 = 64512 at launch
-constexpr int TILE_REGS_FEED = 72, TILE_REGS_SOFTMAX = 208;
+// registers per thread after the split: 128 x 88 + 256 x 208 = 64512, the 384 x 168 of the launch
+constexpr int TILE_REGS_FEED = 88, TILE_REGS_SOFTMAX = 208;
 constexpr uint32_t TILE_TMEM_COLS = 512;
 constexpr float TILE_SLACK = 8.f;      // growth of a row's maximum that needs no rescaling
+#ifndef TPE
+#define TPE 4
+#endif
+constexpr int TILE_POLY_EVERY = TPE;     // every so-manieth pair of exponentials by polynomial
 
 struct PagedTileArgs {
     PagedAttnArgs a;
@@ -122,6 +126,56 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Pairs of fp32 values in one 64-bit register, and the packed instructions on them.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 2^x of two values without the special function unit, whose 16 results a clock would otherwise bound the kernel:
+// x = n + r with n the nearest whole number (adding 1.5 * 2^23 leaves n in the low bits), 2^r on [-1/2, 1/2] by the
+// polynomial of degree 4 with the least largest relative error (2.6e-6, found by iterated reweighted least squares),
+// and n added to the exponent field.  At -126 and below the result is 0 (a masked score, -inf, among them); a NaN
+// does not come back as a small number.
+__device__ __forceinline__ void exp2_poly2(uint64_t x, float &a, float &b) {
+    float x0, x1;
+    unpack2(x, x0, x1);
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x0));   // -126
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x1));
+    const uint64_t xc = pack2(x0, x1), magic = pack2(12582912.f, 12582912.f), back = pack2(-12582912.f, -12582912.f);
+    const uint64_t t = add2(xc, magic);
+    const uint64_t n = add2(t, back);
+    const uint64_t r = fma2(n, pack2(-1.f, -1.f), xc);
+    uint64_t p = fma2(pack2(0.009570102207362652f, 0.009570102207362652f), r, pack2(0.05591785907745361f, 0.05591785907745361f));
+    p = fma2(p, r, pack2(0.240247443318367f, 0.240247443318367f));
+    p = fma2(p, r, pack2(0.6931217908859253f, 0.6931217908859253f));
+    p = fma2(p, r, pack2(0.9999992847442627f, 0.9999992847442627f));
+    float t0, t1, p0, p1;
+    unpack2(t, t0, t1);
+    unpack2(p, p0, p1);
+    a = x0 <= -126.f ? 0.f : __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+    b = x1 <= -126.f ? 0.f : __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
 template <int XT, int D, int PARTS, int KT>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -139,7 +193,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + SM::BARS);
     uint64_t *full = bars, *empty = bars + ST, *q_full = bars + 2 * ST, *s_full = q_full + 2, *p_full = s_full + 2,
-             *o_full = p_full + 2, *all_done = o_full + 2;
+             *o_full = p_full + 4, *all_done = o_full + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(all_done + 1);
 
     // ---- which rows, which kv head, which part of the keys
@@ -197,6 +251,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             mbar_init(&q_full[t], 4);
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
+            mbar_init(&p_full[t + 2], 4);
             mbar_init(&o_full[t], 1);
         }
         mbar_init(all_done, 1);
@@ -258,35 +313,49 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMA
         regs_dec<TILE_REGS_FEED>();
+        // Everything between the arrival of a probability tile and the next products is on the critical path, and
+        // this warp's instructions compete with long straight runs of the softmax warps' for the instruction cache:
+        // descriptors are made once and advanced by adding.
         bool ok = true;
-        auto wait_slot = [&](int i) {
-            return mbar_wait(&full[i % ST], (uint32_t)((i / ST) & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
+        int slot = 0;           // of the ring, and its phase
+        uint32_t phase = 0;
+        auto advance = [&] {
+            if (++slot == ST) {
+                slot = 0;
+                phase ^= 1u;
+            }
         };
-        auto scores = [&](int t, int j) {   // S_t = Q_t K_j^T (one lane)
-            const uint32_t qb = q_smem + t * SM::QB, kb = ring + (uint32_t)((2 * j) % ST) * SM::SLOT;
+        const uint64_t q_desc = umma_desc_sw128(q_smem), k_desc = umma_desc_sw128(ring),
+                       v_desc = umma_desc_mn_sw128(ring, SM::HALF_KV);
+        auto scores = [&](int t, int at) {   // S_t = Q_t K^T, the keys in slot `at`
+            const uint64_t qd = q_desc + (uint64_t)(t * (SM::QB >> 4)), kd = k_desc + (uint64_t)(at * (SM::SLOT >> 4));
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-                umma_f16(s_col(t), umma_desc_sw128(qb + (kk / 4) * SM::HALF_Q + (kk % 4) * 32),
-                         umma_desc_sw128(kb + (kk / 4) * SM::HALF_KV + (kk % 4) * 32), IDESC_S, kk ? 1u : 0u);
+                umma_f16(s_col(t), qd + ((kk / 4) * SM::HALF_Q + (kk % 4) * 32) / 16,
+                         kd + ((kk / 4) * SM::HALF_KV + (kk % 4) * 32) / 16, IDESC_S, kk ? 1u : 0u);
             umma_commit(&s_full[t]);
         };
+        // tiles (of this CTA) that end a segment within: their value rows behind the last key are zeroed
+        const int end_pre = c.prefix_len % KT ? npre - 1 - j0 : -1, end_own = own_load % KT ? nall - 1 - j0 : -1;
         if (cnt > 0) {
-            ok = wait_slot(0);
+            ok = mbar_wait(&full[0], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
             for (int t = 0; ok && t < 2; ++t) {
                 if ((t ? cnt1 : cnt0) == 0) continue;
                 if (!(ok = mbar_wait(&q_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
                 tc_fence_after();
-                if (lane == 0) scores(t, 0);
+                if (elect_one()) scores(t, 0);
             }
-            if (ok && lane == 0) umma_commit(&empty[0]);
+            if (ok && elect_one()) umma_commit(&empty[0]);
+            advance();
             for (int j = 0; ok && j < cnt; ++j) {
-                const int iv = 2 * j + 1;
-                if (!(ok = wait_slot(iv))) break;
-                int key0;
-                const int valid = tile_keys(j0 + j, &key0);
-                if (valid < KT) {
+                if (!(ok = mbar_wait(&full[slot], phase, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                const int v_slot = slot;
+                advance();
+                if (j == end_pre || j == end_own) {
                     // value rows behind the last key hold anything (NaN): zeros, as P is zero there
-                    const uint32_t vb = ring + (uint32_t)(iv % ST) * SM::SLOT;
+                    int key0;
+                    const int valid = tile_keys(j0 + j, &key0);
+                    const uint32_t vb = ring + (uint32_t)v_slot * SM::SLOT;
                     for (int x = lane; x < (KT - valid) * 8; x += 32)
 #pragma unroll
                         for (uint32_t h = 0; h < SM::HALVES; ++h)
@@ -294,34 +363,49 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (j + 1 < cnt && !(ok = wait_slot(iv + 1))) break;
-                for (int t = 0; ok && t < 2; ++t) {
+                const int k_slot = slot;
+                if (j + 1 < cnt) {
+                    if (!(ok = mbar_wait(&full[slot], phase, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                    advance();
+                }
+                const uint64_t vd = v_desc + (uint64_t)(v_slot * (SM::SLOT >> 4));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
                     const int mine = t ? cnt1 : cnt0;
                     if (j >= mine) continue;
-                    if (!(ok = mbar_wait(&p_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t vb = ring + (uint32_t)(iv % ST) * SM::SLOT;
+                    // the probabilities come in two halves, so that the products of the first overlap the
+                    // exponentials of the second
 #pragma unroll
-                        for (int p = PARTS - 1; p >= 0; --p)
+                    for (int half = 0; half < 2; ++half) {
+                        if (ok) ok = mbar_wait(&p_full[t + 2 * half], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < KT / 16; ++kk)
-                                umma_f16_ts(o_col(t), s_col(t) + p * (KT / 2) + kk * 8,
-                                            umma_desc_mn_sw128(vb + kk * 2048, SM::HALF_KV), IDESC_O,
-                                            (j > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
-                        if (j + 1 < mine)
-                            scores(t, j + 1);
-                        else
-                            umma_commit(&o_full[t]);
+                            for (int p = PARTS - 1; p >= 0; --p)
+#pragma unroll
+                                for (int kk = half * KT / 32; kk < (half + 1) * KT / 32; ++kk)
+                                    umma_f16_ts(o_col(t), s_col(t) + p * (KT / 2) + kk * 8, vd + kk * 128, IDESC_O,
+                                                (j > 0 || half > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
+                            if (half == 1) {
+                                if (j + 1 < mine)
+                                    scores(t, k_slot);
+                                else
+                                    umma_commit(&o_full[t]);
+                            }
+                        }
+                        __syncwarp();
                     }
+                    if (!ok) break;
                 }
-                if (ok && lane == 0) {
-                    umma_commit(&empty[iv % ST]);
-                    if (j + 1 < cnt) umma_commit(&empty[(iv + 1) % ST]);
+                if (ok && elect_one()) {
+                    umma_commit(&empty[v_slot]);
+                    if (j + 1 < cnt) umma_commit(&empty[k_slot]);
                 }
             }
         }
-        if (lane == 0) umma_commit(all_done);   // every MMA is over before TMEM is released
+        __syncwarp();
+        if (elect_one()) umma_commit(all_done);   // every MMA is over before TMEM is released
         __syncwarp();
         mbar_wait(all_done, 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
     } else if (warp < 4) {
@@ -334,24 +418,32 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         const int mine = t ? cnt1 : cnt0;
         // Q into shared memory: consecutive threads take consecutive 16 bytes of a row
         if (mine > 0) {
-            constexpr int CH = D / 8;
+            constexpr int CH = D / 8, STEP = TILE_ROWS / CH, N = TILE_ROWS / STEP;
             const uint32_t qb = q_smem + t * SM::QB;
-#pragma unroll 4
-            for (int x = tid; x < TILE_ROWS * CH; x += TILE_ROWS) {
-                const int r = x / CH, ch = x % CH, rr = t * TILE_ROWS + r;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (rr < rows) {
-                    const int ri = rs.row0 + rr;
-                    v = __ldg(reinterpret_cast<const uint4 *>(
-                        a.q + ((size_t)(rs.tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D + 8 * ch));
-                    if (ta.flip) {
-                        v.x ^= 0x80008000u;
-                        v.y ^= 0x80008000u;
-                        v.z ^= 0x80008000u;
-                        v.w ^= 0x80008000u;
-                    }
+            const int ch = tid % CH, r0 = tid / CH;
+            // rows r0, r0 + STEP, ...: their tokens and heads by addition, all the loads in flight at once
+            const int ri = rs.row0 + t * TILE_ROWS + r0, tok_step = STEP / a.G, head_step = STEP % a.G;
+            int tok = ri / a.G, head = ri % a.G;
+            uint4 v[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (t * TILE_ROWS + r0 + i * STEP < rows)
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                        a.q + ((size_t)(rs.tok0 + tok) * a.H + (size_t)g * a.G + head) * D + 8 * ch));
+                tok += tok_step;
+                head += head_step;
+                if (head >= a.G) {
+                    head -= a.G;
+                    ++tok;
                 }
-                st_shared_v4(qb + (ch / 8) * SM::HALF_Q + r * 128 + (((ch % 8) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+            }
+            const uint32_t sign = ta.flip ? 0x80008000u : 0u;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = r0 + i * STEP;
+                st_shared_v4(qb + (ch / 8) * SM::HALF_Q + r * 128 + (((ch % 8) ^ (r & 7)) << 4), v[i].x ^ sign,
+                             v[i].y ^ sign, v[i].z ^ sign, v[i].w ^ sign);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -376,22 +468,30 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             if (!(ok = mbar_wait(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
             tc_fence_after();
             uint32_t s[KT];
-#pragma unroll
-            for (int x = 0; x < KT; x += 32) tmem_ld_32x32b_x32(sc + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
-            tmem_wait_ld();
             int key0;
             tile_keys(j0 + j, &key0);
             const int limit = (j0 + j < npre ? pre : own) - key0;   // keys of the tile that the row sees
-            if (limit < KT) {
-#pragma unroll
-                for (int x = 0; x < KT; ++x)
-                    if (x >= limit) s[x] = 0xff800000u;             // -inf
-            }
-            __syncwarp();
+            const bool cut = __any_sync(0xffffffffu, limit < KT);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int x = 0; x < KT; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.qscale;
+            for (int x = 0; x < 64; x += 32) tmem_ld_32x32b_x32(sc + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
+            tmem_wait_ld();
+            // the second half's scores arrive under the first's maximum
+#pragma unroll
+            for (int x = 64; x < KT; x += 32) tmem_ld_32x32b_x32(sc + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
+#pragma unroll
+            for (int x0 = 0; x0 < KT; x0 += 64) {
+                if (x0 > 0) tmem_wait_ld();
+                if (cut) {
+#pragma unroll
+                    for (int x = x0; x < x0 + 64; ++x)
+                        if (x >= limit) s[x] = 0xff800000u;         // -inf
+                }
+#pragma unroll
+                for (int x = x0; x < x0 + 64; x += 2)
+                    mx[(x / 2) & 3] = max3(mx[(x / 2) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+            }
+            const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.qscale;
             // (the first tile with a live key sets m; O is overwritten by the first product)
             const bool grown = top > m + TILE_SLACK || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grown)) {
@@ -412,19 +512,29 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 }
             }
             const float base = m == -INFINITY ? 0.f : m;            // a row that has seen nothing: all zeros
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t scale2 = pack2(a.qscale, a.qscale), base2 = pack2(-base, -base);
+            uint64_t sum2[2] = {0, 0};
+            // a part of the exponentials by polynomial, where a 16-bit result rounds its error away
 #pragma unroll
             for (int x0 = 0; x0 < KT; x0 += 32) {
                 uint32_t h[16];
 #pragma unroll
                 for (int x = 0; x < 32; x += 2) {
-                    const float p0 = ex2(fmaf(__uint_as_float(s[x0 + x]), a.qscale, -base));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[x0 + x + 1]), a.qscale, -base));
-                    sum[x & 3] += p0;
-                    sum[(x & 3) + 1] += p1;
+                    const uint64_t y = fma2(pack2(__uint_as_float(s[x0 + x]), __uint_as_float(s[x0 + x + 1])), scale2, base2);
+                    float p0, p1;
+                    if (PARTS == 1 && (x / 2) % TILE_POLY_EVERY == TILE_POLY_EVERY - 1) {
+                        exp2_poly2(y, p0, p1);
+                    } else {
+                        unpack2(y, p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                    }
+                    sum2[(x / 2) & 1] = add2(sum2[(x / 2) & 1], pack2(p0, p1));
                     h[x / 2] = pack16<XT>(p0, p1);
-                    s[x0 + x] = __float_as_uint(p0 - lo16<XT>(h[x / 2]));
-                    s[x0 + x + 1] = __float_as_uint(p1 - hi16<XT>(h[x / 2]));
+                    if constexpr (PARTS > 1) {
+                        s[x0 + x] = __float_as_uint(p0 - lo16<XT>(h[x / 2]));
+                        s[x0 + x + 1] = __float_as_uint(p1 - hi16<XT>(h[x / 2]));
+                    }
                 }
                 tmem_st_32x32b_x16(sc + x0 / 2, h);
 #pragma unroll
@@ -438,12 +548,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     }
                     tmem_st_32x32b_x16(sc + p * (KT / 2) + x0 / 2, h);
                 }
+                if (x0 + 32 == KT / 2 || x0 + 32 == KT) {   // a half is ready
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[t + (x0 + 32 == KT ? 2 : 0)]);
+                }
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[t]);
+            float l0, l1;
+            unpack2(add2(sum2[0], sum2[1]), l0, l1);
+            l += l0 + l1;
         }
         // ---------------------------------------------------------- results
         if (mine > 0 && ok) ok = mbar_wait(&o_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);

@@ -89,7 +89,7 @@ constexpr uint32_t kWaitHintNs = 20000;
 // timeout_ns nanoseconds.  Returns false (after setting `errbit` in the device
 // error word) when the bound runs out; the caller then stops its loop.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64_t timeout_ns, unsigned errbit) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
         if (mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
@@ -98,6 +98,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
             return false;
         }
     }
+}
+
+// One lane of a converged warp (always the same one): the compiler knows that a single thread runs what follows.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // --------------------------------------------------------------- cp.async
