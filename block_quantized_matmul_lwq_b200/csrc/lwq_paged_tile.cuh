@@ -13,7 +13,8 @@
 //               a tile is as many boxes as pages it spans
 //   warp 1      tcgen05.mma: S_t = Q_t K^T (both from shared memory), then
 //               O_t += P_t V with P_t in TMEM, over S_t's columns
-//   warps 2, 3  idle (registers are split by groups of four warps)
+//   warp 2      answers for tiles that have landed, and clears the value rows
+//               behind a segment's last key (warp 3 idles)
 //   warps 4..11 softmax, one thread per row: S_t from TMEM, running maximum
 //               and sum in fp32, P_t back to TMEM
 //
@@ -39,10 +40,6 @@ constexpr int TILE_THREADS = 384;
 constexpr int TILE_REGS_FEED = 88, TILE_REGS_SOFTMAX = 208;
 constexpr uint32_t TILE_TMEM_COLS = 512;
 constexpr float TILE_SLACK = 8.f;      // growth of a row's maximum that needs no rescaling
-#ifndef TPE
-#define TPE 4
-#endif
-constexpr int TILE_POLY_EVERY = TPE;     // every so-manieth pair of exponentials by polynomial
 
 struct PagedTileArgs {
     PagedAttnArgs a;
@@ -151,31 +148,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// 2^x of two values without the special function unit, whose 16 results a clock would otherwise bound the kernel:
-// x = n + r with n the nearest whole number (adding 1.5 * 2^23 leaves n in the low bits), 2^r on [-1/2, 1/2] by the
-// polynomial of degree 4 with the least largest relative error (2.6e-6, found by iterated reweighted least squares),
-// and n added to the exponent field.  At -126 and below the result is 0 (a masked score, -inf, among them); a NaN
-// does not come back as a small number.
-__device__ __forceinline__ void exp2_poly2(uint64_t x, float &a, float &b) {
-    float x0, x1;
-    unpack2(x, x0, x1);
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x0));   // -126
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x1));
-    const uint64_t xc = pack2(x0, x1), magic = pack2(12582912.f, 12582912.f), back = pack2(-12582912.f, -12582912.f);
-    const uint64_t t = add2(xc, magic);
-    const uint64_t n = add2(t, back);
-    const uint64_t r = fma2(n, pack2(-1.f, -1.f), xc);
-    uint64_t p = fma2(pack2(0.009570102207362652f, 0.009570102207362652f), r, pack2(0.05591785907745361f, 0.05591785907745361f));
-    p = fma2(p, r, pack2(0.240247443318367f, 0.240247443318367f));
-    p = fma2(p, r, pack2(0.6931217908859253f, 0.6931217908859253f));
-    p = fma2(p, r, pack2(0.9999992847442627f, 0.9999992847442627f));
-    float t0, t1, p0, p1;
-    unpack2(t, t0, t1);
-    unpack2(p, p0, p1);
-    a = x0 <= -126.f ? 0.f : __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-    b = x1 <= -126.f ? 0.f : __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
-
 template <int XT, int D, int PARTS, int KT>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -184,6 +156,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     static_assert(PARTS * KT / 2 <= 128 && KT <= 128 && KT % 64 == 0, "a tile's scores and probabilities share 128 columns");
     static_assert(SM::STAGES >= 3, "K and V of a tile and the next K");
     constexpr int ST = SM::STAGES;
+    constexpr int SPLIT = KT == 128 ? 96 : 32;   // keys of the first part of the probabilities
     constexpr uint32_t IDESC_S = umma_idesc_f16(XT == X_F16 ? 0 : 1, TILE_ROWS, KT);
     constexpr uint32_t IDESC_O = umma_idesc_f16(XT == X_F16 ? 0 : 1, TILE_ROWS, D) | (1u << 16);   // B along N
     extern __shared__ uint8_t raw[];
@@ -250,7 +223,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(&q_full[t], 4);
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 4);
+            mbar_init(&p_full[t], 5);       // four softmax warps, and warp 2
             mbar_init(&p_full[t + 2], 4);
             mbar_init(&o_full[t], 1);
         }
@@ -279,6 +252,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         return min(KT, own_load - *key0);
     };
 
+    // a warp's wait, by one of its lanes (each lane that tries costs the barrier's unit a turn)
+    auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(bar, parity, ta.timeout_ns, DEVERR_ATTN_WAIT);
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    };
     if (warp == 0) {
         // -------------------------------------------------------------- TMA
         regs_dec<TILE_REGS_FEED>();
@@ -298,7 +277,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             }
             for (int w = 0; w < 2; ++w, ++i) {
                 const int slot = i % ST;
-                if (i >= ST && !(ok = mbar_wait(&empty[slot], (uint32_t)((i / ST - 1) & 1), ta.timeout_ns, DEVERR_ATTN_WAIT)))
+                if (i >= ST && !(ok = warp_wait(&empty[slot], (uint32_t)((i / ST - 1) & 1))))
                     break;
                 if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * brows * D * 2));
                 __syncwarp();
@@ -309,105 +288,108 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
         // copies still in flight land before the block ends
         for (int x = max(0, i - ST); x < i; ++x)
-            mbar_wait(&full[x % ST], (uint32_t)((x / ST) & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
+            warp_wait(&full[x % ST], (uint32_t)((x / ST) & 1));
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMA
         regs_dec<TILE_REGS_FEED>();
-        // Everything between the arrival of a probability tile and the next products is on the critical path, and
-        // this warp's instructions compete with long straight runs of the softmax warps' for the instruction cache:
-        // descriptors are made once and advanced by adding.
-        bool ok = true;
-        int slot = 0;           // of the ring, and its phase
-        uint32_t phase = 0;
-        auto advance = [&] {
-            if (++slot == ST) {
-                slot = 0;
-                phase ^= 1u;
-            }
-        };
-        const uint64_t q_desc = umma_desc_sw128(q_smem), k_desc = umma_desc_sw128(ring),
-                       v_desc = umma_desc_mn_sw128(ring, SM::HALF_KV);
-        auto scores = [&](int t, int at) {   // S_t = Q_t K^T, the keys in slot `at`
-            const uint64_t qd = q_desc + (uint64_t)(t * (SM::QB >> 4)), kd = k_desc + (uint64_t)(at * (SM::SLOT >> 4));
+        // One thread.  What lies between the arrival of probabilities and the next products is the critical path, so
+        // it waits for nothing else (warp 2 answers for the tiles in shared memory, as one of the arrivals on the
+        // probabilities' barrier); descriptors are made once and advanced by adding, and a tile's slots are handed
+        // back late, behind the next tile's first products (a commit is not issued before the products ahead of it).
+        if (elect_one()) {
+            bool ok = true;
+            int slot = 0;           // of the ring
+            const uint64_t q_desc = umma_desc_sw128(q_smem), k_desc = umma_desc_sw128(ring),
+                           v_desc = umma_desc_mn_sw128(ring, SM::HALF_KV);
+            auto scores = [&](int t, int at) {   // S_t = Q_t K^T, the keys in slot `at`
+                const uint64_t qd = q_desc + (uint64_t)(t * (SM::QB >> 4)), kd = k_desc + (uint64_t)(at * (SM::SLOT >> 4));
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                umma_f16(s_col(t), qd + ((kk / 4) * SM::HALF_Q + (kk % 4) * 32) / 16,
-                         kd + ((kk / 4) * SM::HALF_KV + (kk % 4) * 32) / 16, IDESC_S, kk ? 1u : 0u);
-            umma_commit(&s_full[t]);
-        };
-        // tiles (of this CTA) that end a segment within: their value rows behind the last key are zeroed
-        const int end_pre = c.prefix_len % KT ? npre - 1 - j0 : -1, end_own = own_load % KT ? nall - 1 - j0 : -1;
-        if (cnt > 0) {
-            ok = mbar_wait(&full[0], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
-            for (int t = 0; ok && t < 2; ++t) {
-                if ((t ? cnt1 : cnt0) == 0) continue;
-                if (!(ok = mbar_wait(&q_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
-                tc_fence_after();
-                if (elect_one()) scores(t, 0);
-            }
-            if (ok && elect_one()) umma_commit(&empty[0]);
-            advance();
-            for (int j = 0; ok && j < cnt; ++j) {
-                if (!(ok = mbar_wait(&full[slot], phase, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
-                const int v_slot = slot;
-                advance();
-                if (j == end_pre || j == end_own) {
-                    // value rows behind the last key hold anything (NaN): zeros, as P is zero there
-                    int key0;
-                    const int valid = tile_keys(j0 + j, &key0);
-                    const uint32_t vb = ring + (uint32_t)v_slot * SM::SLOT;
-                    for (int x = lane; x < (KT - valid) * 8; x += 32)
-#pragma unroll
-                        for (uint32_t h = 0; h < SM::HALVES; ++h)
-                            st_shared_v4(vb + h * SM::HALF_KV + (uint32_t)(valid * 128 + x * 16), 0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_f16(s_col(t), qd + ((kk / 4) * SM::HALF_Q + (kk % 4) * 32) / 16,
+                             kd + ((kk / 4) * SM::HALF_KV + (kk % 4) * 32) / 16, IDESC_S, kk ? 1u : 0u);
+                umma_commit(&s_full[t]);
+            };
+            int back[2] = {-1, -1};   // slots to hand back
+            if (cnt > 0) {
+                ok = mbar_wait(&full[0], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+                for (int t = 0; ok && t < 2; ++t) {
+                    if ((t ? cnt1 : cnt0) == 0) continue;
+                    if (!(ok = mbar_wait(&q_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                    scores(t, 0);
                 }
-                const int k_slot = slot;
-                if (j + 1 < cnt) {
-                    if (!(ok = mbar_wait(&full[slot], phase, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
-                    advance();
-                }
-                const uint64_t vd = v_desc + (uint64_t)(v_slot * (SM::SLOT >> 4));
+                back[0] = 0;
+                for (int j = 0; ok && j < cnt; ++j) {
+                    const int v_slot = slot + 1 < ST ? slot + 1 : 0, k_slot = v_slot + 1 < ST ? v_slot + 1 : 0;
+                    slot = k_slot;
+                    const uint64_t vd = v_desc + (uint64_t)(v_slot * (SM::SLOT >> 4));
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int mine = t ? cnt1 : cnt0;
-                    if (j >= mine) continue;
-                    // the probabilities come in two halves, so that the products of the first overlap the
-                    // exponentials of the second
+                    for (int t = 0; t < 2; ++t) {
+                        const int mine = t ? cnt1 : cnt0;
+                        if (!ok || j >= mine) continue;
+                        // the probabilities come in two parts, so that the products of the first overlap the
+                        // exponentials of the second
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        if (ok) ok = mbar_wait(&p_full[t + 2 * half], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
+                        for (int part = 0; part < 2; ++part) {
+                            if (ok) ok = mbar_wait(&p_full[t + 2 * part], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
+                            if (!ok) continue;
+                            tc_fence_after();
 #pragma unroll
                             for (int p = PARTS - 1; p >= 0; --p)
 #pragma unroll
-                                for (int kk = half * KT / 32; kk < (half + 1) * KT / 32; ++kk)
+                                for (int kk = part ? SPLIT / 16 : 0; kk < (part ? KT / 16 : SPLIT / 16); ++kk)
                                     umma_f16_ts(o_col(t), s_col(t) + p * (KT / 2) + kk * 8, vd + kk * 128, IDESC_O,
-                                                (j > 0 || half > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
-                            if (half == 1) {
-                                if (j + 1 < mine)
-                                    scores(t, k_slot);
-                                else
-                                    umma_commit(&o_full[t]);
+                                                (j > 0 || part > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
+                            if (part == 0) {
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    if (back[i] >= 0) umma_commit(&empty[back[i]]);
+                                    back[i] = -1;
+                                }
                             }
                         }
-                        __syncwarp();
+                        if (!ok) continue;
+                        if (j + 1 < mine)
+                            scores(t, k_slot);
+                        else
+                            umma_commit(&o_full[t]);
                     }
-                    if (!ok) break;
-                }
-                if (ok && elect_one()) {
-                    umma_commit(&empty[v_slot]);
-                    if (j + 1 < cnt) umma_commit(&empty[k_slot]);
+                    back[0] = v_slot;
+                    back[1] = j + 1 < cnt ? k_slot : -1;
                 }
             }
+            umma_commit(all_done);   // every MMA is over before TMEM is released
+            mbar_wait(all_done, 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
         }
         __syncwarp();
-        if (elect_one()) umma_commit(all_done);   // every MMA is over before TMEM is released
-        __syncwarp();
-        mbar_wait(all_done, 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+    } else if (warp == 2) {
+        // -------------------------------------------------- tiles that landed
+        regs_dec<TILE_REGS_FEED>();
+        // V_j and K_(j+1) are in, and the value rows behind a segment's last key, which hold anything (NaN), are zeros
+        // (P is zero there): an arrival on both row tiles' probability barriers
+        const int end_pre = c.prefix_len % KT ? npre - 1 - j0 : -1, end_own = own_load % KT ? nall - 1 - j0 : -1;
+        bool ok = true;
+        for (int j = 0; ok && j < cnt; ++j) {
+            const int iv = 2 * j + 1;
+            if (!(ok = warp_wait(&full[iv % ST], (uint32_t)((iv / ST) & 1)))) break;
+            if (j == end_pre || j == end_own) {
+                int key0;
+                const int valid = tile_keys(j0 + j, &key0);
+                const uint32_t vb = ring + (uint32_t)(iv % ST) * SM::SLOT;
+                for (int x = lane; x < (KT - valid) * 8; x += 32)
+#pragma unroll
+                    for (uint32_t h = 0; h < SM::HALVES; ++h)
+                        st_shared_v4(vb + h * SM::HALF_KV + (uint32_t)(valid * 128 + x * 16), 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (j + 1 < cnt && !(ok = warp_wait(&full[(iv + 1) % ST], (uint32_t)(((iv + 1) / ST) & 1)))) break;
+            for (int t = 0; ok && t < 2; ++t) {
+                if (j >= (t ? cnt1 : cnt0)) continue;
+                // (this phase's arrival only once the last phase is over)
+                if (j > 0 && !(ok = warp_wait(&p_full[t], (uint32_t)((j - 1) & 1)))) break;
+                if (lane == 0) mbar_arrive(&p_full[t]);
+            }
+        }
     } else if (warp < 4) {
         regs_dec<TILE_REGS_FEED>();
     } else {
@@ -514,7 +496,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             const float base = m == -INFINITY ? 0.f : m;            // a row that has seen nothing: all zeros
             const uint64_t scale2 = pack2(a.qscale, a.qscale), base2 = pack2(-base, -base);
             uint64_t sum2[2] = {0, 0};
-            // a part of the exponentials by polynomial, where a 16-bit result rounds its error away
 #pragma unroll
             for (int x0 = 0; x0 < KT; x0 += 32) {
                 uint32_t h[16];
@@ -522,13 +503,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 for (int x = 0; x < 32; x += 2) {
                     const uint64_t y = fma2(pack2(__uint_as_float(s[x0 + x]), __uint_as_float(s[x0 + x + 1])), scale2, base2);
                     float p0, p1;
-                    if (PARTS == 1 && (x / 2) % TILE_POLY_EVERY == TILE_POLY_EVERY - 1) {
-                        exp2_poly2(y, p0, p1);
-                    } else {
-                        unpack2(y, p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                    }
+                    unpack2(y, p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
                     sum2[(x / 2) & 1] = add2(sum2[(x / 2) & 1], pack2(p0, p1));
                     h[x / 2] = pack16<XT>(p0, p1);
                     if constexpr (PARTS > 1) {
@@ -548,7 +525,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     }
                     tmem_st_32x32b_x16(sc + p * (KT / 2) + x0 / 2, h);
                 }
-                if (x0 + 32 == KT / 2 || x0 + 32 == KT) {   // a half is ready
+                if (x0 + 32 == SPLIT || x0 + 32 == KT) {   // a part is ready
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -560,7 +537,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             l += l0 + l1;
         }
         // ---------------------------------------------------------- results
-        if (mine > 0 && ok) ok = mbar_wait(&o_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+        if (mine > 0 && ok) ok = warp_wait(&o_full[t], 0);
         tc_fence_after();
         if (ok) {
             float *pp = nullptr;
