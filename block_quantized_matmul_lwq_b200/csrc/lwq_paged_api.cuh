@@ -128,23 +128,25 @@ int paged_workspace(int dev, size_t need, void **ws) {
 constexpr int kDecodeCtasPerSm = 2;
 
 template <int XT, int D, int NG, int PARTS>
-cudaError_t launch_paged_decode(const PagedDecodeArgs &d, const PagedCombineArgs &k, cudaStream_t st) {
+cudaError_t launch_paged_decode(const PagedPrefixArgs &k, cudaStream_t st) {
     auto kern = paged_decode_kernel<XT, D, NG, PARTS>;
     constexpr size_t smem = PagedDecodeSmem<D, NG>::TOTAL;
+    const PagedDecodeArgs &d = k.d;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
     if ((e = launch_k(kern, d.ctas, PD_WARPS * 32, smem, st, false, d)) != cudaSuccess) return e;
-    return launch_k(paged_combine_kernel<XT, D>, d.a.c.B * d.a.H, PC_THREADS, 0, st, true, k);
+    if (!k.prefix) return launch_k(paged_combine_kernel<XT, D>, d.ctas * d.a.G, PC_THREADS, 0, st, true, d);
+    return launch_k(paged_prefix_combine_kernel<XT, D>, (int)(((long)d.a.c.B * d.a.H + 7) / 8), 256, 0, st, true, k);
 }
 template <int XT, int D, int PARTS>
-cudaError_t launch_paged_decode_g(const PagedDecodeArgs &d, const PagedCombineArgs &k, cudaStream_t st) {
-    return d.a.G <= 8 ? launch_paged_decode<XT, D, 1, PARTS>(d, k, st) : launch_paged_decode<XT, D, 2, PARTS>(d, k, st);
+cudaError_t launch_paged_decode_g(const PagedPrefixArgs &k, cudaStream_t st) {
+    return k.d.a.G <= 8 ? launch_paged_decode<XT, D, 1, PARTS>(k, st) : launch_paged_decode<XT, D, 2, PARTS>(k, st);
 }
 // fp16's two parts of a probability hold 22 bits; bf16 takes a third part for an fp32 result
 template <int D>
-cudaError_t launch_paged_decode_x(int dtype, const PagedDecodeArgs &d, const PagedCombineArgs &k, cudaStream_t st) {
-    if (dtype == LWQ_ACT_F16) return launch_paged_decode_g<X_F16, D, 2>(d, k, st);
-    return d.a.out16 ? launch_paged_decode_g<X_BF16, D, 2>(d, k, st) : launch_paged_decode_g<X_BF16, D, 3>(d, k, st);
+cudaError_t launch_paged_decode_x(int dtype, const PagedPrefixArgs &k, cudaStream_t st) {
+    if (dtype == LWQ_ACT_F16) return launch_paged_decode_g<X_F16, D, 2>(k, st);
+    return k.d.a.out16 ? launch_paged_decode_g<X_BF16, D, 2>(k, st) : launch_paged_decode_g<X_BF16, D, 3>(k, st);
 }
 
 // -------------------------------------------------------------- row tiles
@@ -217,19 +219,20 @@ void prefill_plan(const lwq_paged *c, int T, int H, int sms, long *pairs, int *s
     *splits = tile_splits(*pairs, c->Hkv, (long)c->max_pages * c->page + c->prefix_len, sms);
 }
 
-// The parts of a decode call's workspace: the CTAs' slots, then, with a prefix, one result per (sequence, head) and
-// the prefix's partial results.
+// The parts of a decode call's workspace: the CTAs' slots and the list of pairs that several CTAs work on, then, with a
+// prefix, one result per (sequence, head) and the prefix's partial results.
 struct DecodeSpace {
-    size_t slots, whole, prefix;
+    size_t slots, list, whole, prefix;
     long pairs;
     int splits;
-    size_t total() const { return slots + whole + prefix; }
+    size_t total() const { return slots + list + whole + prefix; }
 };
 DecodeSpace decode_space(const lwq_paged *c, int H, int sms) {
     DecodeSpace s;
     const int G = H / c->Hkv;
     const size_t ps = part_stride(c->D) * sizeof(float);
     s.slots = (size_t)kDecodeCtasPerSm * sms * 2 * G * ps;
+    s.list = (size_t)kDecodeCtasPerSm * sms * sizeof(int4);
     s.whole = s.prefix = 0;
     s.pairs = 0;
     s.splits = 0;
@@ -364,17 +367,18 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
     void *ws;
     if ((rc = paged_workspace(dev, sp.total(), &ws))) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    PagedCombineArgs k;
+    PagedPrefixArgs k;
     PagedDecodeArgs &d = k.d;
     d.a = a;
     d.slots = static_cast<float *>(ws);
+    d.splits = reinterpret_cast<int4 *>(static_cast<uint8_t *>(ws) + sp.slots);
     d.whole = nullptr;
     d.ctas = kDecodeCtasPerSm * sm_count(dev);
     k.prefix = nullptr;
     k.splits = 0;
     int launches = 2;
     if (cache->prefix_len > 0) {
-        d.whole = d.slots + sp.slots / sizeof(float);
+        d.whole = d.slots + (sp.slots + sp.list) / sizeof(float);
         k.splits = sp.splits;
         float *part = d.whole + sp.whole / sizeof(float);
         k.prefix = part;
@@ -385,8 +389,8 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
             return rc;
         ++launches;
     }
-    const cudaError_t e = cache->D == 64 ? launch_paged_decode_x<64>(cache->dtype, d, k, st)
-                                         : launch_paged_decode_x<128>(cache->dtype, d, k, st);
+    const cudaError_t e = cache->D == 64 ? launch_paged_decode_x<64>(cache->dtype, k, st)
+                                         : launch_paged_decode_x<128>(cache->dtype, k, st);
     if (e != cudaSuccess) return LWQ_ERR_CUDA;
     t_last_launches = launches;
     return LWQ_OK;

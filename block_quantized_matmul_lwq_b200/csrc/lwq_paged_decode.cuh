@@ -7,7 +7,8 @@
 // ragged lengths, a single long sequence and a large batch all fill the GPU,
 // and the host needs to know none of the lengths.  A run may begin or end
 // inside a pair; such a pair's partial results (running maximum, sum, weighted
-// values) go to the workspace and a second kernel merges them.
+// values) go to the workspace and a second kernel merges them, told by the CTA
+// in whose run the pair begins how many there are.
 //
 // Within a CTA each of the 4 warps takes 16 of a unit's 64 keys (one page, as
 // pages are at least 16 tokens) through its own cp.async ring, which runs
@@ -48,39 +49,13 @@ struct Runs {
     }
 };
 
-// Units per kv head before sequence b (returned to every thread), and of the
-// whole batch, by all threads of the block.
-__device__ __forceinline__ void units_before(const PagedArgs &c, int b, long *before, long *all) {
-    __shared__ long sb[32], sa[32];
-    long x = 0, y = 0;
-    for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
-        const int n = units_of(own_len(c, i));
-        y += n;
-        if (i < b) x += n;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-        y += __shfl_xor_sync(0xffffffffu, y, o);
-    }
-    if ((threadIdx.x & 31) == 0) {
-        sb[threadIdx.x >> 5] = x;
-        sa[threadIdx.x >> 5] = y;
-    }
-    __syncthreads();
-    x = y = 0;
-    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) {
-        x += sb[i];
-        y += sa[i];
-    }
-    *before = x;
-    *all = y;
-}
-
 struct PagedDecodeArgs {
     PagedAttnArgs a;
     float *slots;       // [ctas][2][G] partial results of a CTA's first and last pair
-    float *whole;       // [B][H] results of pairs that one CTA finished, when a prefix is still to be added
+    int4 *splits;       // [ctas]: the pair (x: sequence, y: kv head) that begins in this run and ends in a later one;
+                        // z: the CTAs that it spans (0: there is none), w: the first one's slot
+    float *whole;       // [B][H] results of pairs that one CTA finished, when a prefix is still to be added; for any
+                        // other pair, words 2 and 3 hold z and 2 * CTA + w of its entry above
     int ctas;
 };
 
@@ -132,6 +107,22 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
     const long total = scan.all * c.Hkv;
     const Runs runs(total, d.ctas);
     const long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);
+    if (threadIdx.x == 0) d.splits[blockIdx.x] = make_int4(0, 0, 0, 0);   // (this thread also writes the last word on it)
+    // sequences with no token of their own: zeros, or nothing beside the prefix
+    for (int b = blockIdx.x; b < c.B; b += d.ctas) {
+        if (own_len(c, b) > 0) continue;
+        for (int x = threadIdx.x; x < a.H * D; x += PD_WARPS * 32) {
+            if (!d.whole) {
+                if (a.out16)
+                    static_cast<uint16_t *>(a.out)[(size_t)b * a.H * D + x] = 0;
+                else
+                    static_cast<float *>(a.out)[(size_t)b * a.H * D + x] = 0.f;
+            } else if (x < a.H) {
+                *reinterpret_cast<float4 *>(d.whole + ((size_t)b * a.H + x) * part_stride(D)) =
+                    make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            }
+        }
+    }
     if (u0 >= u1) return;
     UnitPos cur;
     long before;
@@ -346,12 +337,19 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
                 } else {
                     float *pp = complete ? d.whole + bh * part_stride(D)
                                          : d.slots + (((size_t)blockIdx.x * 2 + (pair > 0)) * G + h) * part_stride(D);
-                    if (e == 0) {
-                        pp[0] = M;
-                        pp[1] = L;
-                    }
+                    if (e == 0) *reinterpret_cast<float4 *>(pp) = make_float4(M, L, 0.f, 0.f);
                     pp[4 + e] = A;
                 }
+            }
+            if (!end_of_pair && (pair > 0 || i + 1 == cur.u + 1)) {
+                // the pair begins in this run (`i + 1 == cur.u + 1`: with its first unit) and goes on in later ones
+                const long end = u1 + (cur.n - 1 - cur.u);   // past its last unit
+                const int count = runs.cta_of(end - 1) - (int)blockIdx.x + 1, slot = pair > 0;
+                if (threadIdx.x == 0) d.splits[blockIdx.x] = make_int4(cur.b, cur.g, count, slot);
+                if (d.whole && threadIdx.x < G)
+                    *reinterpret_cast<float4 *>(d.whole + ((size_t)cur.b * a.H + (size_t)cur.g * G + threadIdx.x) *
+                                                              part_stride(D)) =
+                        make_float4(0.f, 0.f, __int_as_float(count), __int_as_float(2 * blockIdx.x + slot));
             }
             __syncthreads();   // the merge space is free again
             ++pair;
@@ -362,98 +360,115 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
     pdl_launch_dependents();
 }
 
-// Merges partial results: one block per (sequence, query head), D columns by
-// blockDim.x / D groups of threads, each group taking every so-manieth partial.
-// The partials of a pair are, in this order: the prefix's splits, then the
-// pair's own -- the slots of the CTAs whose runs it spans, or the result of the
-// one CTA that finished it.  The order of every addition is fixed by the sizes.
-struct PagedCombineArgs {
-    PagedDecodeArgs d;
-    const float *prefix;     // [(row / 256 * Hkv + g) * splits + s][256] rows, row = b G + h; or null
-    int splits;
-};
-constexpr int PC_THREADS = 512;
+// One step of a merge: a partial result (m, l, one value) joins (M, L, A).
+template <int E>
+__device__ __forceinline__ void merge_part(float &M, float &L, float (&A)[E], float m, float l, const float (&v)[E]) {
+    if (m == -INFINITY) return;
+    const float mn = fmaxf(M, m), fo = exp2f(M - mn), fn = exp2f(m - mn);   // fo = 0 while M = -inf
+    L = fmaf(L, fo, l * fn);
+#pragma unroll
+    for (int e = 0; e < E; ++e) A[e] = fmaf(A[e], fo, v[e] * fn);
+    M = mn;
+}
+template <int XT>
+__device__ __forceinline__ void store_out(const PagedAttnArgs &a, size_t at, float v) {
+    if (a.out16)
+        static_cast<uint16_t *>(a.out)[at] = (uint16_t)pack16<XT>(v, 0.f);
+    else
+        static_cast<float *>(a.out)[at] = v;
+}
 
+// Merges the pairs that several CTAs worked on: a block per (CTA in whose run
+// a pair begins, query head), D columns by groups of threads that take every
+// so-manieth partial result.  The order of every addition is fixed by the
+// sizes.  Most blocks have nothing to do.
+constexpr int PC_THREADS = 512;
 template <int XT, int D>
-__global__ void __launch_bounds__(PC_THREADS) paged_combine_kernel(const PagedCombineArgs k) {
-    constexpr int NGR = PC_THREADS / D, PS = part_stride(D);
+__global__ void __launch_bounds__(PC_THREADS) paged_combine_kernel(const PagedDecodeArgs d) {
+    constexpr int NGR = PC_THREADS / D, PS = part_stride(D), U = 4;
     __shared__ float gm[NGR], gl[NGR], go[NGR][D];
-    const PagedAttnArgs &a = k.d.a;
-    const PagedArgs &c = a.c;
-    const int b = blockIdx.x / a.H, hh = blockIdx.x % a.H, g = hh / a.G, h = hh % a.G;
-    long before, all;
-    units_before(c, b, &before, &all);
-    const int n = units_of(own_len(c, b));
+    const PagedAttnArgs &a = d.a;
+    const int i0 = blockIdx.x / a.G, h = blockIdx.x % a.G;
     pdl_wait();
-    // the CTAs whose runs meet this pair's units [first, first + n)
-    int i0 = 0, own = 0;
-    bool whole = false, inner = false;
-    if (n > 0) {
-        const long total = all * c.Hkv, first = before * c.Hkv + (long)g * n;
-        const Runs runs(total, k.d.ctas);
-        i0 = runs.cta_of(first);
-        own = runs.cta_of(first + n - 1) - i0 + 1;
-        whole = own == 1;
-        inner = runs.start(i0) < first;   // the first CTA began in an earlier pair
-        if (whole && !k.prefix) return;                    // written already
-    }
-    const int count = (k.prefix ? k.splits : 0) + own;
-    const int pre = count - own;
+    const int4 sp = __ldcg(d.splits + i0);
+    if (sp.z == 0) return;
     const int e = threadIdx.x % D, grp = threadIdx.x / D;
-    const size_t row = (size_t)b * a.G + h;
-    auto slot = [&](int i) -> const float * {
-        if (i < pre) return k.prefix + ((((row >> 8) * c.Hkv + g) * k.splits + i) * 256 + (row & 255)) * PS;
-        i -= pre;
-        if (whole) return k.d.whole + ((size_t)b * a.H + hh) * PS;
-        return k.d.slots + (((size_t)(i0 + i) * 2 + (i == 0 && inner)) * a.G + h) * PS;
-    };
-    float M = -INFINITY, L = 0.f, A = 0.f;
-    constexpr int U = 4;
-    for (int s0 = grp; s0 < count; s0 += NGR * U) {
-        float mv[U], lv[U], av[U];
+    float M = -INFINITY, L = 0.f, A[1] = {0.f};
+    for (int s0 = grp; s0 < sp.z; s0 += NGR * U) {
+        float mv[U], lv[U], av[U][1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * NGR;
-            mv[u] = -INFINITY;
-            if (s < count) {
-                const float *p = slot(s);
-                mv[u] = __ldcg(p);
-                lv[u] = __ldcg(p + 1);
-                av[u] = __ldcg(p + 4 + e);
-            }
+            const float *p = d.slots + (((size_t)(i0 + (s < sp.z ? s : 0)) * 2 + (s == 0 ? sp.w : 0)) * a.G + h) * PS;
+            mv[u] = s < sp.z ? __ldcg(p) : -INFINITY;
+            lv[u] = __ldcg(p + 1);
+            av[u][0] = __ldcg(p + 4 + e);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (mv[u] == -INFINITY) continue;
-            const float mn = fmaxf(M, mv[u]), fo = exp2f(M - mn), fn = exp2f(mv[u] - mn);
-            L = fmaf(L, fo, lv[u] * fn);
-            A = fmaf(A, fo, av[u] * fn);
-            M = mn;
-        }
+        for (int u = 0; u < U; ++u) merge_part(M, L, A, mv[u], lv[u], av[u]);
     }
     if (e == 0) {
         gm[grp] = M;
         gl[grp] = L;
     }
-    go[grp][e] = A;
+    go[grp][e] = A[0];
     __syncthreads();
     if (grp) return;
-    float Mt = -INFINITY, Lt = 0.f, At = 0.f;
-#pragma unroll
-    for (int i = 0; i < NGR; ++i) Mt = fmaxf(Mt, gm[i]);
+    float Mt = -INFINITY, Lt = 0.f, At[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NGR; ++i) {
-        if (gm[i] == -INFINITY) continue;
-        const float f = exp2f(gm[i] - Mt);
-        Lt = fmaf(gl[i], f, Lt);
-        At = fmaf(go[i][e], f, At);
+        const float v[1] = {go[i][e]};
+        merge_part(Mt, Lt, At, gm[i], gl[i], v);
     }
-    const float r = Lt > 0.f ? At / Lt : 0.f;   // no token at all: zeros
-    const size_t at = ((size_t)b * a.H + hh) * D + e;
-    if (a.out16)
-        static_cast<uint16_t *>(a.out)[at] = (uint16_t)pack16<XT>(r, 0.f);
-    else
-        static_cast<float *>(a.out)[at] = r;
+    store_out<XT>(a, ((size_t)sp.x * a.H + (size_t)sp.y * a.G + h) * D + e, At[0] / Lt);
+}
+
+// Adds the prefix's partial results to each row's own: a warp per (sequence,
+// query head), its lanes the columns.
+struct PagedPrefixArgs {
+    PagedDecodeArgs d;
+    const float *prefix;     // [(row / 256 * Hkv + g) * splits + s][256] rows, row = b G + h
+    int splits;
+};
+template <int XT, int D>
+__global__ void __launch_bounds__(256) paged_prefix_combine_kernel(const PagedPrefixArgs k) {
+    constexpr int E = D / 32, PS = part_stride(D), U = 4;
+    const PagedAttnArgs &a = k.d.a;
+    const long w = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    if (w >= (long)a.c.B * a.H) return;
+    const int b = (int)(w / a.H), hh = (int)(w % a.H), g = hh / a.G, h = hh % a.G;
+    const long row = (long)b * a.G + h;
+    const float *pre = k.prefix + ((((row >> 8) * a.c.Hkv + g) * k.splits) * 256 + (row & 255)) * PS;
+    const float *own = k.d.whole + (size_t)w * PS;
+    const float4 head = __ldcg(reinterpret_cast<const float4 *>(own));
+    const int count = __float_as_int(head.z), first = __float_as_int(head.w);
+    float M = -INFINITY, L = 0.f, A[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) A[e] = 0.f;
+    const int total = k.splits + (count ? count : 1);
+    for (int s0 = 0; s0 < total; s0 += U) {
+        float mv[U], lv[U], av[U][E];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u, o = s - k.splits;
+            const float *p = pre;
+            if (s < k.splits)
+                p = pre + (size_t)s * 256 * PS;
+            else if (s < total)
+                p = count == 0 ? own : k.d.slots + (((size_t)(first / 2 + o) * 2 + (o == 0 ? first & 1 : 0)) * a.G + h) * PS;
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p));
+            mv[u] = s < total ? ml.x : -INFINITY;
+            lv[u] = ml.y;
+#pragma unroll
+            for (int e = 0; e < E; ++e) av[u][e] = __ldcg(p + 4 + 32 * e + lane);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) merge_part(M, L, A, mv[u], lv[u], av[u]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) store_out<XT>(a, (size_t)w * D + 32 * e + lane, A[e] / L);   // the prefix has a token
 }
 
 }  // namespace lwq

@@ -29,7 +29,7 @@
 // rounding); an fp32 result takes two in fp16 (22 bits), three in bf16 (24).
 #pragma once
 
-#include "lwq_paged.cuh"
+#include "lwq_paged_decode.cuh"
 
 namespace lwq {
 
@@ -622,34 +622,19 @@ __global__ void __launch_bounds__(256) paged_tile_combine_kernel(const PagedTile
         float mv[U], lv[U], av[U][E];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            mv[u] = -INFINITY;
-            if (s0 + u < ta.splits) {
-                const float *p = p0 + (size_t)(s0 + u) * PAIR_ROWS * PS;
-                mv[u] = __ldcg(p);
-                lv[u] = __ldcg(p + 1);
+            const float *p = p0 + (size_t)(s0 + u < ta.splits ? s0 + u : 0) * PAIR_ROWS * PS;
+            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p));
+            mv[u] = s0 + u < ta.splits ? ml.x : -INFINITY;
+            lv[u] = ml.y;
 #pragma unroll
-                for (int e = 0; e < E; ++e) av[u][e] = __ldcg(p + 4 + 32 * e + lane);
-            }
+            for (int e = 0; e < E; ++e) av[u][e] = __ldcg(p + 4 + 32 * e + lane);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (mv[u] == -INFINITY) continue;
-            const float mn = fmaxf(M, mv[u]), fo = exp2f(M - mn), fn = exp2f(mv[u] - mn);
-            L = fmaf(L, fo, lv[u] * fn);
-#pragma unroll
-            for (int e = 0; e < E; ++e) A[e] = fmaf(A[e], fo, av[u][e] * fn);
-            M = mn;
-        }
+        for (int u = 0; u < U; ++u) merge_part(M, L, A, mv[u], lv[u], av[u]);
     }
     const size_t at = ((size_t)(tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float v = L > 0.f ? A[e] / L : 0.f;
-        if (a.out16)
-            static_cast<uint16_t *>(a.out)[at + 32 * e + lane] = (uint16_t)pack16<XT>(v, 0.f);
-        else
-            static_cast<float *>(a.out)[at + 32 * e + lane] = v;
-    }
+    for (int e = 0; e < E; ++e) store_out<XT>(a, at + 32 * e + lane, L > 0.f ? A[e] / L : 0.f);
 }
 
 }  // namespace lwq
