@@ -78,6 +78,7 @@ class lwq_paged(ctypes.Structure):
         super().__init__(_ptr(k), _ptr(v), _ptr(tables), _ptr(lens), _ptr(prefix), prefix_len, act, B, Hkv, D, page,
                          max_pages, num_pages)
         self.owners = (k, v, tables, lens, prefix)
+        self.at = ctypes.addressof(self)
 
 
 class lwq_rope(ctypes.Structure):
@@ -85,6 +86,10 @@ class lwq_rope(ctypes.Structure):
 
     _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("axes", ctypes.c_int),
                 ("reserved", ctypes.c_int), ("turn", ctypes.c_uint64 * 64), ("axis", ctypes.c_uint8 * 64)]
+
+    def __init__(self):
+        super().__init__()
+        self.at = ctypes.addressof(self)
 
 
 def _load() -> ctypes.CDLL:
@@ -113,9 +118,9 @@ def _load() -> ctypes.CDLL:
     lib.lwq_attention_workspace_size.argtypes = [i, i, i, i, i]
     lib.lwq_attention_decode.restype = i
     lib.lwq_attention_decode.argtypes = [i, vp, vp, vp, vp, vp, i, i, i, i, i, c.c_float, vp]
-    pc, pr, i64 = c.POINTER(lwq_paged), c.POINTER(lwq_rope), c.c_int64
+    pc, pr, i64 = vp, vp, c.c_int64   # structs by address (lwq_paged.at, lwq_rope.at): cheaper per call than byref
     lib.lwq_rope_init.restype = i
-    lib.lwq_rope_init.argtypes = [pr, i, i, c.c_double, c.POINTER(c.c_double), i, c.POINTER(i)]
+    lib.lwq_rope_init.argtypes = [c.POINTER(lwq_rope), i, i, c.c_double, c.POINTER(c.c_double), i, c.POINTER(i)]
     lib.lwq_kv_append.restype = i
     lib.lwq_kv_append.argtypes = [pc, pr, i, vp, i64, vp, i64, vp, i64, vp, vp, vp, i, i, vp]
     lib.lwq_attention_paged_workspace_size.restype = c.c_size_t
@@ -141,7 +146,9 @@ def lib() -> ctypes.CDLL:
 
 class _LazyLib:
     def __getattr__(self, name):
-        return getattr(lib(), name)
+        f = getattr(lib(), name)
+        setattr(self, name, f)   # later calls find it as a plain attribute
+        return f
 
 
 _lib = _LazyLib()
@@ -260,27 +267,27 @@ def lwq_rope_init(rot_dim: int, base: float = 10000.0, layout: int = LWQ_ROPE_HA
 def lwq_kv_append(cache: lwq_paged, rope, src: int, q, ldq: int, k, ldk: int, v, ldv: int, q_out, T: int, H: int,
                   cu_tokens=None, positions=None, stream=None) -> None:
     """Rotate q and k by position (rope None: not) and store k and v in the cache (see include/lwq.h)."""
-    _check(_lib.lwq_kv_append(ctypes.byref(cache), None if rope is None else ctypes.byref(rope), src, _ptr(q), ldq,
+    _check(_lib.lwq_kv_append(cache.at, None if rope is None else rope.at, src, _ptr(q), ldq,
                               _ptr(k), ldk, _ptr(v), ldv, _ptr(q_out), _ptr(cu_tokens), _ptr(positions), T, H,
                               _stream(stream)), "lwq_kv_append")
 
 
 def lwq_attention_paged_workspace_size(cache: lwq_paged, H: int) -> int:
-    return _lib.lwq_attention_paged_workspace_size(ctypes.byref(cache), H)
+    return _lib.lwq_attention_paged_workspace_size(cache.at, H)
 
 
 def lwq_attention_paged(cache: lwq_paged, q, out, H: int, scale: float, flags: int = 0, stream=None) -> None:
     """Decode attention, one query token per sequence, over the paged cache and its shared prefix."""
-    _check(_lib.lwq_attention_paged(ctypes.byref(cache), flags, _ptr(q), _ptr(out), H, float(scale),
+    _check(_lib.lwq_attention_paged(cache.at, flags, _ptr(q), _ptr(out), H, float(scale),
                                     _stream(stream)), "lwq_attention_paged")
 
 
 def lwq_attention_prefill_workspace_size(cache: lwq_paged, T: int, H: int) -> int:
-    return _lib.lwq_attention_prefill_workspace_size(ctypes.byref(cache), T, H)
+    return _lib.lwq_attention_prefill_workspace_size(cache.at, T, H)
 
 
 def lwq_attention_prefill(cache: lwq_paged, q, out, cu_tokens, T: int, H: int, scale: float, flags: int = 0,
                           stream=None) -> None:
     """Causal attention of the batch's new tokens over the cache that already holds them."""
-    _check(_lib.lwq_attention_prefill(ctypes.byref(cache), flags, _ptr(q), _ptr(out), _ptr(cu_tokens), T, H,
+    _check(_lib.lwq_attention_prefill(cache.at, flags, _ptr(q), _ptr(out), _ptr(cu_tokens), T, H,
                                       float(scale), _stream(stream)), "lwq_attention_prefill")

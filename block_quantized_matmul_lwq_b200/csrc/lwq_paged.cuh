@@ -56,7 +56,6 @@ __device__ __forceinline__ size_t cache_row(const PagedArgs &c, int p, int g, in
 // bits, as a signed fraction of a half turn, go to sincospi.  So a position of
 // 2^31 costs no accuracy (fp32 angles would be off by whole turns there), and
 // no 64-bit floating point is used.
-constexpr int APPEND_ITERS = 4;
 constexpr int APPEND_WARPS = 4;
 
 struct AppendArgs {
@@ -92,7 +91,7 @@ __device__ __forceinline__ void store4(uint16_t *p, const float (&f)[4]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack16<XT>(f[0], f[1]), pack16<XT>(f[2], f[3]));
 }
 
-template <int ST, int XT, int D>
+template <int ST, int XT, int D, int APPEND_ITERS>
 __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const AppendArgs a, const lwq_rope rope) {
     constexpr int LPH = D / 8;          // lanes per head
     constexpr int HPI = 32 / LPH;       // heads per warp access
@@ -101,41 +100,13 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
     const int t = (int)(w / a.units), unit = (int)(w % a.units);
     if (t >= a.T) return;
     const PagedArgs &c = a.c;
-    // the token's sequence b: the number of sequences that end at or before it
-    int b = t, idx = 0, n = 1;
-    if (a.cu) {
-        int cnt = 0;
-        for (int i = lane; i < c.B; i += 32) cnt += __ldg(a.cu + i + 1) <= t;
-        b = __reduce_add_sync(0xffffffffu, cnt);
-        if (b >= c.B) return;           // behind the last sequence
-        const int t0 = __ldg(a.cu + b);
-        idx = t - t0;
-        n = __ldg(a.cu + b + 1) - t0;
-    }
-    const long place = (long)__ldg(c.lens + b) - n + idx;
-    if (idx < 0 || idx >= n || place < 0) return;   // padding
     const int pi = lane % LPH, sub = lane / LPH;
     const bool turned = a.rope && 8 * pi < rope.rot_dim;
     const bool halves = turned && !a.pairs_layout;
     // element offsets of the lane's two groups of four
     const int e0 = halves ? 4 * pi : 8 * pi;
     const int e1 = halves ? e0 + rope.rot_dim / 2 : e0 + 4;
-    float cs[4], sn[4];
-    if (turned) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = a.positions ? __ldg(a.positions + (size_t)rope.axis[4 * pi + i] * a.T + t)
-                                      : c.prefix_len + (int)place;
-            const uint64_t turns = (uint64_t)(int64_t)p * rope.turn[4 * pi + i];
-            const int half_turns = (int)(uint32_t)((turns + 0x80000000ull) >> 32);
-            sincospif((float)half_turns * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31
-        }
-    }
-    int page = -1;
-    if (place < (long)c.max_pages * c.page)
-        page = page_of(c, c.tables + (size_t)b * c.max_pages, (int)place);
-    else
-        set_dev_error(DEVERR_BAD_PAGE);
+    // the rows first: what follows looks up the token's place while they are on their way
     const int hq = a.q ? a.H : 0, heads = hq + 2 * c.Hkv;
     const int h0 = unit * APPEND_ITERS * HPI + sub;
     float x[APPEND_ITERS][2][4];
@@ -152,6 +123,46 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
         load4<ST>(row, e0, x[i][0]);
         load4<ST>(row, e1, x[i][1]);
     }
+    // the token's sequence b, its tokens' first row and count, and its length: a lane looks at one sequence, all three
+    // words at once, so that only the page table's word waits for another
+    int b = t, idx = 0, n = 1, len = 0;
+    if (a.cu) {
+        bool found = false;
+        for (int i0 = 0; i0 < c.B && !found; i0 += 32) {
+            const int i = min(i0 + lane, c.B - 1);
+            const int lo = __ldg(a.cu + i), hi = __ldg(a.cu + i + 1), ln = __ldg(c.lens + i);
+            const unsigned hit = __ballot_sync(0xffffffffu, t >= lo && t < hi);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                b = min(i0 + at, c.B - 1);
+                idx = t - __shfl_sync(0xffffffffu, lo, at);
+                n = __shfl_sync(0xffffffffu, hi - lo, at);
+                len = __shfl_sync(0xffffffffu, ln, at);
+                found = true;
+            }
+        }
+        if (!found) return;             // behind the last sequence
+    } else {
+        len = __ldg(c.lens + b);
+    }
+    const long place = (long)len - n + idx;
+    if (place < 0) return;              // padding
+    float cs[4], sn[4];
+    if (turned) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = a.positions ? __ldg(a.positions + (size_t)rope.axis[4 * pi + i] * a.T + t)
+                                      : c.prefix_len + (int)place;
+            const uint64_t turns = (uint64_t)(int64_t)p * rope.turn[4 * pi + i];
+            const int half_turns = (int)(uint32_t)((turns + 0x80000000ull) >> 32);
+            sincospif((float)half_turns * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31
+        }
+    }
+    int page = -1;
+    if (place < (long)c.max_pages * c.page)
+        page = page_of(c, c.tables + (size_t)b * c.max_pages, (int)place);
+    else
+        set_dev_error(DEVERR_BAD_PAGE);
 #pragma unroll
     for (int i = 0; i < APPEND_ITERS; ++i) {
         const int h = h0 + i * HPI;

@@ -78,18 +78,21 @@ int rope_check(const lwq_rope *r, int D) {
 }
 
 template <int ST, int XT>
-cudaError_t launch_append(int D, const AppendArgs &a, const lwq_rope &rope, unsigned blocks, cudaStream_t st) {
+cudaError_t launch_append(int D, int iters, const AppendArgs &a, const lwq_rope &rope, unsigned blocks, cudaStream_t st) {
+    constexpr int N = APPEND_WARPS * 32;
     if (D == 64)
-        kv_append_kernel<ST, XT, 64><<<blocks, APPEND_WARPS * 32, 0, st>>>(a, rope);
+        iters == 8 ? kv_append_kernel<ST, XT, 64, 8><<<blocks, N, 0, st>>>(a, rope)
+                   : kv_append_kernel<ST, XT, 64, 4><<<blocks, N, 0, st>>>(a, rope);
     else
-        kv_append_kernel<ST, XT, 128><<<blocks, APPEND_WARPS * 32, 0, st>>>(a, rope);
+        iters == 8 ? kv_append_kernel<ST, XT, 128, 8><<<blocks, N, 0, st>>>(a, rope)
+                   : kv_append_kernel<ST, XT, 128, 4><<<blocks, N, 0, st>>>(a, rope);
     return cudaGetLastError();
 }
 template <int ST>
-cudaError_t launch_append_xt(int dtype, int D, const AppendArgs &a, const lwq_rope &rope, unsigned blocks,
+cudaError_t launch_append_xt(int dtype, int D, int iters, const AppendArgs &a, const lwq_rope &rope, unsigned blocks,
                              cudaStream_t st) {
-    return dtype == LWQ_ACT_F16 ? launch_append<ST, X_F16>(D, a, rope, blocks, st)
-                                : launch_append<ST, X_BF16>(D, a, rope, blocks, st);
+    return dtype == LWQ_ACT_F16 ? launch_append<ST, X_F16>(D, iters, a, rope, blocks, st)
+                                : launch_append<ST, X_BF16>(D, iters, a, rope, blocks, st);
 }
 
 // The checks that both attention calls make, and the kernels' view of the arguments.
@@ -134,7 +137,8 @@ cudaError_t launch_paged_decode(const PagedPrefixArgs &k, cudaStream_t st) {
     const PagedDecodeArgs &d = k.d;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
-    if ((e = launch_k(kern, d.ctas, PD_WARPS * 32, smem, st, false, d)) != cudaSuccess) return e;
+    // behind a prefix's row tiles: a dependent launch that starts as their CTAs end and waits for the last of them at its own end
+    if ((e = launch_k(kern, d.ctas, PD_WARPS * 32, smem, st, k.prefix != nullptr, d)) != cudaSuccess) return e;
     if (!k.prefix) return launch_k(paged_combine_kernel<XT, D>, d.ctas * d.a.G, PC_THREADS, 0, st, true, d);
     return launch_k(paged_prefix_combine_kernel<XT, D>, (int)(((long)d.a.c.B * d.a.H + 7) / 8), 256, 0, st, true, k);
 }
@@ -171,7 +175,7 @@ int launch_paged_tile(const lwq_paged *c, PagedTileArgs &t, long pairs, cudaStre
     if (launch_k(kern, (int)(pairs * c->Hkv * t.splits), TILE_THREADS, smem, st, false, maps[0], maps[1], t) != cudaSuccess)
         return LWQ_ERR_CUDA;
     if (t.prefix_only || t.splits == 1) return LWQ_OK;
-    return launch_k(paged_tile_combine_kernel<XT, D>, (int)(pairs * c->Hkv * (PAIR_ROWS / 8)), 256, 0, st, true, t) ==
+    return launch_k(paged_tile_combine_kernel<XT, D>, (int)(((long)t.a.T * t.a.H + 7) / 8), 256, 0, st, true, t) ==
                    cudaSuccess
                ? LWQ_OK
                : LWQ_ERR_CUDA;
@@ -323,8 +327,11 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
     a.positions = positions;
     a.T = T;
     a.H = H;
-    const int per = APPEND_ITERS * (256 / D);   // heads per warp
-    a.units = ((q ? H : 0) + 2 * cache->Hkv + per - 1) / per;
+    // rows of heads per warp: 8 when that still leaves the GPU a few thousand warps (a prompt), else 4
+    const int heads = (q ? H : 0) + 2 * cache->Hkv, wide = 8 * (256 / D);
+    const int iters = (double)T * ((heads + wide - 1) / wide) >= 4096.0 ? 8 : 4;
+    const int per = iters * (256 / D);          // heads per warp
+    a.units = (heads + per - 1) / per;
     const double warps = (double)T * a.units;
     if (warps > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
     a.rope = rope ? 1 : 0;
@@ -338,11 +345,11 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (src == LWQ_ACT_F32)
-        e = launch_append_xt<X_F32>(cache->dtype, D, a, r, blocks, st);
+        e = launch_append_xt<X_F32>(cache->dtype, D, iters, a, r, blocks, st);
     else if (src == LWQ_ACT_F16)
-        e = launch_append_xt<X_F16>(cache->dtype, D, a, r, blocks, st);
+        e = launch_append_xt<X_F16>(cache->dtype, D, iters, a, r, blocks, st);
     else
-        e = launch_append_xt<X_BF16>(cache->dtype, D, a, r, blocks, st);
+        e = launch_append_xt<X_BF16>(cache->dtype, D, iters, a, r, blocks, st);
     if (e != cudaSuccess) return LWQ_ERR_CUDA;
     t_last_launches = 1;
     return LWQ_OK;
@@ -418,7 +425,7 @@ int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void
     long pairs;
     int splits;
     prefill_plan(cache, T, H, sm_count(dev), &pairs, &splits);
-    if ((double)pairs * cache->Hkv * splits * (PAIR_ROWS / 8) > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
+    if ((double)pairs * cache->Hkv * splits > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
     void *ws;
     if ((rc = paged_workspace(dev, splits > 1 ? tile_part_bytes(pairs, cache->Hkv, splits, cache->D) : 0, &ws))) return rc;
     PagedTileArgs t = paged_tile_args(cache, a, splits, static_cast<float *>(ws));

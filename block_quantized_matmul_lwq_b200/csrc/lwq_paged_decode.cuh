@@ -123,7 +123,10 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
             }
         }
     }
-    if (u0 >= u1) return;
+    if (u0 >= u1) {
+        pdl_wait();
+        return;
+    }
     UnitPos cur;
     long before;
     scan.locate(u0 / c.Hkv, scratch, &cur.b, &before, units);
@@ -174,31 +177,36 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
 
     uint32_t qa[D / 16][2 * NG];
     float o[NG][D / 8][4], m[NG], l[NG];
-    bool fresh = true;
+    // Q as the A operand: MMA row r is query head r of the kv head (rows >= G are zero)
+    auto load_q = [&](const UnitPos &p) {
+#pragma unroll
+        for (int gg = 0; gg < NG; ++gg) {
+            const int h = 8 * gg + gr;
+            const uint16_t *qr = a.q + ((size_t)p.b * a.H + (size_t)p.g * G + (h < G ? h : 0)) * D;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t x0 = __ldg(reinterpret_cast<const unsigned int *>(qr + 16 * ks + 2 * t));
+                const uint32_t x1 = __ldg(reinterpret_cast<const unsigned int *>(qr + 16 * ks + 8 + 2 * t));
+                qa[ks][2 * gg] = h < G ? x0 : 0u;
+                qa[ks][2 * gg + 1] = h < G ? x1 : 0u;
+            }
+        }
+    };
+    auto clear = [&] {
+#pragma unroll
+        for (int gg = 0; gg < NG; ++gg) {
+            m[gg] = -INFINITY;
+            l[gg] = 0.f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[gg][n][e] = 0.f;
+        }
+    };
+    load_q(cur);
+    clear();
     int pair = 0;   // pairs of this run so far
     for (int i = 0; i < steps; ++i) {
-        if (fresh) {
-            // Q as the A operand: MMA row r is query head r of the kv head (rows >= G are zero)
-#pragma unroll
-            for (int gg = 0; gg < NG; ++gg) {
-                const int h = 8 * gg + gr;
-                const uint16_t *qr = a.q + ((size_t)cur.b * a.H + (size_t)cur.g * G + (h < G ? h : 0)) * D;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t x0 = __ldg(reinterpret_cast<const unsigned int *>(qr + 16 * ks + 2 * t));
-                    const uint32_t x1 = __ldg(reinterpret_cast<const unsigned int *>(qr + 16 * ks + 8 + 2 * t));
-                    qa[ks][2 * gg] = h < G ? x0 : 0u;
-                    qa[ks][2 * gg + 1] = h < G ? x1 : 0u;
-                }
-                m[gg] = -INFINITY;
-                l[gg] = 0.f;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[gg][n][e] = 0.f;
-            }
-            fresh = false;
-        }
         issue(i + ST - 1);
         cp_async_wait<ST - 1>();
         __syncwarp();   // every lane's copies of step i are in and visible to the warp
@@ -295,7 +303,10 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
         __syncwarp();   // the stage is read before a later step's copies refill it
 
         const bool end_of_pair = cur.u + 1 == cur.n, last = i + 1 == steps;
+        UnitPos next = cur;
+        next_unit(c, next);
         if (end_of_pair || last) {
+            if (!last) load_q(next);   // the next pair's queries arrive under the merge
             // merge the warps: per head the largest running maximum, the others rescaled to it
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) {
@@ -353,11 +364,12 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
             }
             __syncthreads();   // the merge space is free again
             ++pair;
-            fresh = true;
+            clear();
         }
-        next_unit(c, cur);
+        cur = next;
     }
     pdl_launch_dependents();
+    pdl_wait();   // a prefix's row tiles, which this kernel does not read, end before it does
 }
 
 // One step of a merge: a partial result (m, l, one value) joins (M, L, A).

@@ -54,6 +54,14 @@ struct PagedTileArgs {
 // pairs of row tiles of a sequence with n new tokens
 __host__ __device__ __forceinline__ long pairs_of(long n, int G) { return n <= 0 ? 0 : (n * G + PAIR_ROWS - 1) / PAIR_ROWS; }
 
+// The tokens of sequence b: its first row of q, and how many (none where cu does not ascend, none past T).
+__device__ __forceinline__ int first_token(const PagedAttnArgs &a, int b) {
+    return a.cu ? min(max(__ldg(a.cu + b), 0), a.T) : b;
+}
+__device__ __forceinline__ int token_count(const PagedAttnArgs &a, int b) {
+    return a.cu ? max(min(__ldg(a.cu + b + 1), a.T) - first_token(a, b), 0) : 1;
+}
+
 // The rows of one pair: its sequence, first row, and what its rows see.
 struct RowSet {
     int b, tok0, n;     // sequence, its first token's row of q, its tokens
@@ -156,6 +164,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     static_assert(PARTS * KT / 2 <= 128 && KT <= 128 && KT % 64 == 0, "a tile's scores and probabilities share 128 columns");
     static_assert(SM::STAGES >= 3, "K and V of a tile and the next K");
     constexpr int ST = SM::STAGES;
+    constexpr int FRESH = PARTS > 1 ? 1024 / KT : 1 << 30;   // key tiles after which O starts anew
     constexpr int SPLIT = KT == 128 ? 96 : 32;   // keys of the first part of the probabilities
     constexpr uint32_t IDESC_S = umma_idesc_f16(XT == X_F16 ? 0 : 1, TILE_ROWS, KT);
     constexpr uint32_t IDESC_O = umma_idesc_f16(XT == X_F16 ? 0 : 1, TILE_ROWS, D) | (1u << 16);   // B along N
@@ -184,17 +193,13 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         pl = pair;
     } else {
         long *scratch = reinterpret_cast<long *>(sm);
-        auto tokens = [&](int b) {
-            if (!a.cu) return 1;
-            const int lo = min(max(__ldg(a.cu + b), 0), a.T), hi = min(__ldg(a.cu + b + 1), a.T);
-            return max(hi - lo, 0);
-        };
-        RunScan<TILE_THREADS> scan(c.B, scratch, [&](int b) { return pairs_of(tokens(b), a.G); });
+        if (threadIdx.x < c.B) asm volatile("prefetch.global.L1 [%0];" ::"l"(c.lens + threadIdx.x));
+        RunScan<TILE_THREADS> scan(c.B, scratch, [&](int b) { return pairs_of(token_count(a, b), a.G); });
         if (pair >= scan.all) return;
         long before;
-        scan.locate(pair, scratch, &rs.b, &before, [&](int b) { return pairs_of(tokens(b), a.G); });
-        rs.tok0 = a.cu ? min(max(__ldg(a.cu + rs.b), 0), a.T) : rs.b;
-        rs.n = tokens(rs.b);
+        scan.locate(pair, scratch, &rs.b, &before, [&](int b) { return pairs_of(token_count(a, b), a.G); });
+        rs.tok0 = first_token(a, rs.b);
+        rs.n = token_count(a, rs.b);
         rs.len = __ldg(c.lens + rs.b);
         pl = pairs_of(rs.n, a.G) - 1 - (pair - before);   // the rows that see most first
         __syncthreads();                                   // the scratch is shared memory of the tiles
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 #pragma unroll
                                 for (int kk = part ? SPLIT / 16 : 0; kk < (part ? KT / 16 : SPLIT / 16); ++kk)
                                     umma_f16_ts(o_col(t), s_col(t) + p * (KT / 2) + kk * 8, vd + kk * 128, IDESC_O,
-                                                (j > 0 || part > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
+                                                (j % FRESH > 0 || part > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
                             if (part == 0) {
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
@@ -445,10 +450,45 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
         const uint32_t sc = s_col(t) + lane_off, oc = o_col(t) + lane_off;
         float m = -INFINITY, l = 0.f;
+        // the row's place in fp32: a partial result's values, or the output's (kept is the maximum its sums refer to)
+        float *row32 = nullptr, kept = -INFINITY;
+        const int ri = rs.row0 + r;
+        const size_t at = live ? ((size_t)(rs.tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D : 0;
+        if (ta.part)
+            row32 = ta.part + (((size_t)(pair * c.Hkv + g) * ta.splits + split) * PAIR_ROWS + r) * part_stride(D) + 4;
+        else if (!a.out16)
+            row32 = static_cast<float *>(a.out) + at;
         bool ok = true;
         for (int j = 0; j < mine; ++j) {
             if (!(ok = mbar_wait(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
             tc_fence_after();
+            const bool fresh = PARTS > 1 && j > 0 && j % FRESH == 0;
+            if (fresh) {
+                // O's sums of the last tiles join those kept (the tensor core is done with O: it has formed S since)
+                const float f = kept == -INFINITY ? 0.f : ex2(kept - m);
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    float4 k[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        k[y] = live && j > FRESH ? *reinterpret_cast<const float4 *>(row32 + x + 4 * y)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(oc + x, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        k[y].x = fmaf(k[y].x, f, __uint_as_float(o[4 * y]));
+                        k[y].y = fmaf(k[y].y, f, __uint_as_float(o[4 * y + 1]));
+                        k[y].z = fmaf(k[y].z, f, __uint_as_float(o[4 * y + 2]));
+                        k[y].w = fmaf(k[y].w, f, __uint_as_float(o[4 * y + 3]));
+                        if (live) *reinterpret_cast<float4 *>(row32 + x + 4 * y) = k[y];
+                    }
+                }
+                __syncwarp();
+                kept = m;
+            }
             uint32_t s[KT];
             int key0;
             tile_keys(j0 + j, &key0);
@@ -481,7 +521,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 const float f = grown ? ex2(m - mn) : 1.f;          // 0 while m = -inf
                 m = mn;
                 l *= f;
-                if (j > 0) {
+                if (j > 0 && !fresh) {
 #pragma unroll
                     for (int x = 0; x < D; x += 32) {
                         uint32_t o[32];
@@ -540,12 +580,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (mine > 0 && ok) ok = warp_wait(&o_full[t], 0);
         tc_fence_after();
         if (ok) {
-            float *pp = nullptr;
-            if (ta.part)
-                pp = ta.part + (((size_t)(pair * c.Hkv + g) * ta.splits + split) * PAIR_ROWS + r) * part_stride(D);
-            if (pp && live) *reinterpret_cast<float2 *>(pp) = make_float2(m, l);
-            const int ri = rs.row0 + r;
-            const size_t at = live ? ((size_t)(rs.tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D : 0;
+            if (ta.part && live) *reinterpret_cast<float2 *>(row32 - 4) = make_float2(m, l);
+            const bool more = PARTS > 1 && mine > FRESH;        // sums were kept
+            const float fk = more && kept != -INFINITY ? ex2(kept - m) : 0.f;
             const float inv = ta.part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
 #pragma unroll
             for (int x0 = 0; x0 < D; x0 += 32) {
@@ -561,7 +598,19 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 if (!live) continue;
                 float f[32];
 #pragma unroll
-                for (int x = 0; x < 32; ++x) f[x] = l > 0.f ? __uint_as_float(o[x]) * inv : 0.f;
+                for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(o[x]);
+                if (more) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        const float4 k = *reinterpret_cast<const float4 *>(row32 + x0 + x);
+                        f[x] = fmaf(k.x, fk, f[x]);
+                        f[x + 1] = fmaf(k.y, fk, f[x + 1]);
+                        f[x + 2] = fmaf(k.z, fk, f[x + 2]);
+                        f[x + 3] = fmaf(k.w, fk, f[x + 3]);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < 32; ++x) f[x] = l > 0.f ? f[x] * inv : 0.f;
                 if (!ta.part && a.out16) {
                     uint16_t *dst = static_cast<uint16_t *>(a.out) + at + x0;
 #pragma unroll
@@ -570,7 +619,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                             make_uint4(pack16<XT>(f[x], f[x + 1]), pack16<XT>(f[x + 2], f[x + 3]),
                                        pack16<XT>(f[x + 4], f[x + 5]), pack16<XT>(f[x + 6], f[x + 7]));
                 } else {
-                    float *dst = ta.part ? pp + 4 + x0 : static_cast<float *>(a.out) + at + x0;
+                    float *dst = row32 + x0;
 #pragma unroll
                     for (int x = 0; x < 32; x += 4)
                         *reinterpret_cast<float4 *>(dst + x) = make_float4(f[x], f[x + 1], f[x + 2], f[x + 3]);
@@ -587,32 +636,40 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     }
 }
 
-// Merges the key splits of a prefill: a warp per (row, kv head), its lanes the
-// columns; the splits in order, eight loads in flight.
+// Merges the key splits of a prefill: a warp per (token, query head), its lanes
+// the columns.
 template <int XT, int D>
 __global__ void __launch_bounds__(256) paged_tile_combine_kernel(const PagedTileArgs ta) {
     constexpr int PS = part_stride(D), E = D / 32, U = 4;
     const PagedAttnArgs &a = ta.a;
     const PagedArgs &c = a.c;
-    __shared__ long scratch[16];
     const int lane = threadIdx.x & 31;
-    const long item = blockIdx.x / (PAIR_ROWS / 8);       // (pair, kv head)
-    const int r = (int)(blockIdx.x % (PAIR_ROWS / 8)) * 8 + (threadIdx.x >> 5);
-    const int g = (int)(item % c.Hkv);
-    const long pair = item / c.Hkv;
-    auto tokens = [&](int b) {
-        if (!a.cu) return 1;
-        const int lo = min(max(__ldg(a.cu + b), 0), a.T), hi = min(__ldg(a.cu + b + 1), a.T);
-        return max(hi - lo, 0);
-    };
-    RunScan<256> scan(c.B, scratch, [&](int b) { return pairs_of(tokens(b), a.G); });
-    if (pair >= scan.all) return;
-    int b;
-    long before;
-    scan.locate(pair, scratch, &b, &before, [&](int b) { return pairs_of(tokens(b), a.G); });
-    const int n = tokens(b), tok0 = a.cu ? min(max(__ldg(a.cu + b), 0), a.T) : b;
-    const long ri = (pairs_of(n, a.G) - 1 - (pair - before)) * PAIR_ROWS + r;
-    if (ri >= (long)n * a.G) return;
+    const long w = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int t = (int)(w / a.H), hh = (int)(w % a.H), g = hh / a.G;
+    if (t >= a.T) return;
+    // the token's sequence, and the pairs of row tiles before it
+    int b = 0, tok0 = 0, n = 0;
+    long before = 0;
+    for (int i0 = 0; i0 < c.B; i0 += 32) {
+        const int i = i0 + lane;
+        const int lo = i < c.B ? first_token(a, i) : 0, k = i < c.B ? token_count(a, i) : 0;
+        const unsigned hit = __ballot_sync(0xffffffffu, k > 0 && t >= lo && t < lo + k);
+        const int at = hit ? __ffs(hit) - 1 : 32;
+        long sum = lane < at ? pairs_of(k, a.G) : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        before += sum;
+        if (hit) {
+            b = i0 + at;
+            tok0 = __shfl_sync(0xffffffffu, lo, at);
+            n = __shfl_sync(0xffffffffu, k, at);
+            break;
+        }
+    }
+    if (n == 0) return;   // behind the last sequence
+    const long ri = (long)(t - tok0) * a.G + hh % a.G;
+    const long pair = before + pairs_of(n, a.G) - 1 - ri / PAIR_ROWS;
+    const int r = (int)(ri % PAIR_ROWS);
     pdl_wait();
     const float *p0 = ta.part + (((size_t)(pair * c.Hkv + g) * ta.splits) * PAIR_ROWS + r) * PS;
     float M = -INFINITY, L = 0.f, A[E];
@@ -632,9 +689,8 @@ __global__ void __launch_bounds__(256) paged_tile_combine_kernel(const PagedTile
 #pragma unroll
         for (int u = 0; u < U; ++u) merge_part(M, L, A, mv[u], lv[u], av[u]);
     }
-    const size_t at = ((size_t)(tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D;
 #pragma unroll
-    for (int e = 0; e < E; ++e) store_out<XT>(a, at + 32 * e + lane, L > 0.f ? A[e] / L : 0.f);
+    for (int e = 0; e < E; ++e) store_out<XT>(a, (size_t)w * D + 32 * e + lane, L > 0.f ? A[e] / L : 0.f);
 }
 
 }  // namespace lwq

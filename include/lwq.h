@@ -326,7 +326,7 @@ int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const do
  * Arithmetic is fp32, each result rounded once to nearest (so a value past
  * fp16's range becomes infinite there).  Tokens from cu_tokens[B] on, and
  * tokens whose place in the cache would be negative (lens[b] 0), are padding:
- * nothing is read or written for them.  A place beyond max_pages * page is
+ * nothing is written for them.  A place beyond max_pages * page is
  * reported as LWQ_ERR_BAD_PAGE and its k and v are dropped.  Two tokens of a
  * call may not share a place in the cache.  One kernel, no workspace.
  * Errors: LWQ_ERR_INVALID_ARG (sizes, NULL pointers, T != B without
