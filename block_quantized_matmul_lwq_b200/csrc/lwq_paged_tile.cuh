@@ -464,26 +464,34 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             tc_fence_after();
             const bool fresh = PARTS > 1 && j > 0 && j % FRESH == 0;
             if (fresh) {
-                // O's sums of the last tiles join those kept (the tensor core is done with O: it has formed S since)
+                // O's sums of the last tiles join those kept (the tensor core is done with O: it has formed S since).
+                // With the maximum unchanged since, as it mostly is, that is an addition in memory, which is not
+                // waited for; the row is this thread's alone, so the order of additions is fixed.
                 const float f = kept == -INFINITY ? 0.f : ex2(kept - m);
+                const int how = j == FRESH ? 0 : __all_sync(0xffffffffu, f == 1.f || !live) ? 1 : 2;
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
-                    float4 k[8];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y)
-                        k[y] = live && j > FRESH ? *reinterpret_cast<const float4 *>(row32 + x + 4 * y)
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
                     uint32_t o[32];
                     __syncwarp();
                     tmem_ld_32x32b_x32(oc + x, o);
                     tmem_wait_ld();
+                    if (!live) continue;
+                    float *p = row32 + x;
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        k[y].x = fmaf(k[y].x, f, __uint_as_float(o[4 * y]));
-                        k[y].y = fmaf(k[y].y, f, __uint_as_float(o[4 * y + 1]));
-                        k[y].z = fmaf(k[y].z, f, __uint_as_float(o[4 * y + 2]));
-                        k[y].w = fmaf(k[y].w, f, __uint_as_float(o[4 * y + 3]));
-                        if (live) *reinterpret_cast<float4 *>(row32 + x + 4 * y) = k[y];
+                    for (int y = 0; y < 32; y += 4) {
+                        float4 v = make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]), __uint_as_float(o[y + 2]),
+                                               __uint_as_float(o[y + 3]));
+                        if (how == 1) {
+                            asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + y), "f"(v.x),
+                                         "f"(v.y), "f"(v.z), "f"(v.w)
+                                         : "memory");
+                            continue;
+                        }
+                        if (how == 2) {
+                            const float4 k = __ldcg(reinterpret_cast<const float4 *>(p + y));
+                            v = make_float4(fmaf(k.x, f, v.x), fmaf(k.y, f, v.y), fmaf(k.z, f, v.z), fmaf(k.w, f, v.w));
+                        }
+                        __stcg(reinterpret_cast<float4 *>(p + y), v);
                     }
                 }
                 __syncwarp();
@@ -602,7 +610,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 if (more) {
 #pragma unroll
                     for (int x = 0; x < 32; x += 4) {
-                        const float4 k = *reinterpret_cast<const float4 *>(row32 + x0 + x);
+                        const float4 k = __ldcg(reinterpret_cast<const float4 *>(row32 + x0 + x));
                         f[x] = fmaf(k.x, fk, f[x]);
                         f[x + 1] = fmaf(k.y, fk, f[x + 1]);
                         f[x + 2] = fmaf(k.z, fk, f[x + 2]);
