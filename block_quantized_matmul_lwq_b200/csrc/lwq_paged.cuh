@@ -46,16 +46,18 @@ __device__ __forceinline__ size_t cache_row(const PagedArgs &c, int p, int g, in
 //
 // A group of D / 8 lanes takes one head of a token: 4 pairs per lane, i.e. 4 + 4
 // (HALF) or 8 (PAIRS) consecutive elements, so that each warp-wide access is
-// whole 128-byte lines; a warp takes APPEND_ITERS such rows of one token with
-// all their loads in flight before the first store, and its lanes' four
-// (cos, sin) are computed once for all of them.  Small row counts per warp keep
-// a single token spread over several warps (48 heads of 128: 6 warps).
+// whole 128-byte lines; a warp takes 4 such accesses of one token's queries,
+// keys or values with all their loads in flight before the first store, and its
+// lanes' four (cos, sin) are computed once for all of them.  So a single token
+// is spread over several warps (40 rotated and 8 other heads of 128: 6 warps),
+// and no warp decides anything per head.
 //
 // The angle position * f is kept in turns as a 64-bit fraction: the low 64 bits
 // of position * turn are the exact product modulo one turn, and their top 32
 // bits, as a signed fraction of a half turn, go to sincospi.  So a position of
 // 2^31 costs no accuracy (fp32 angles would be off by whole turns there), and
 // no 64-bit floating point is used.
+constexpr int APPEND_ITERS = 4;
 constexpr int APPEND_WARPS = 4;
 
 struct AppendArgs {
@@ -64,7 +66,8 @@ struct AppendArgs {
     long ldq, ldk, ldv;
     uint16_t *q_out;
     const int *cu, *positions;
-    int T, H, units;   // units: warps per token
+    int T, H;
+    int uq, uk;        // warps per token for q, and for k (and as many for v)
     int rope;          // 0: no rotation
     int pairs_layout;  // LWQ_ROPE_PAIRS
 };
@@ -91,37 +94,35 @@ __device__ __forceinline__ void store4(uint16_t *p, const float (&f)[4]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack16<XT>(f[0], f[1]), pack16<XT>(f[2], f[3]));
 }
 
-template <int ST, int XT, int D, int APPEND_ITERS>
+template <int ST, int XT, int D>
 __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const AppendArgs a, const lwq_rope rope) {
     constexpr int LPH = D / 8;          // lanes per head
     constexpr int HPI = 32 / LPH;       // heads per warp access
     const int lane = threadIdx.x & 31;
     const long w = (long)blockIdx.x * APPEND_WARPS + (threadIdx.x >> 5);
-    const int t = (int)(w / a.units), unit = (int)(w % a.units);
+    const int units = a.uq + 2 * a.uk, t = (int)(w / units);
+    int unit = (int)(w % units);
     if (t >= a.T) return;
     const PagedArgs &c = a.c;
-    const int pi = lane % LPH, sub = lane / LPH;
-    const bool turned = a.rope && 8 * pi < rope.rot_dim;
+    const int what = unit < a.uq ? 0 : unit < a.uq + a.uk ? 1 : 2;   // q, k, v
+    unit -= what == 0 ? 0 : what == 1 ? a.uq : a.uq + a.uk;
+    const int pi = lane % LPH, h0 = unit * APPEND_ITERS * HPI + lane / LPH, heads = what ? c.Hkv : a.H;
+    const bool turned = a.rope && what < 2 && 8 * pi < rope.rot_dim;
     const bool halves = turned && !a.pairs_layout;
     // element offsets of the lane's two groups of four
     const int e0 = halves ? 4 * pi : 8 * pi;
     const int e1 = halves ? e0 + rope.rot_dim / 2 : e0 + 4;
     // the rows first: what follows looks up the token's place while they are on their way
-    const int hq = a.q ? a.H : 0, heads = hq + 2 * c.Hkv;
-    const int h0 = unit * APPEND_ITERS * HPI + sub;
+    const long ld = what == 0 ? a.ldq : what == 1 ? a.ldk : a.ldv;
+    const char *src = static_cast<const char *>(what == 0 ? a.q : what == 1 ? a.k : a.v) +
+                      (t * ld + (long)h0 * D) * (ST == X_F32 ? 4 : 2);
     float x[APPEND_ITERS][2][4];
 #pragma unroll
     for (int i = 0; i < APPEND_ITERS; ++i) {
-        const int h = h0 + i * HPI;
-        if (h >= heads) break;
-        const long es = ST == X_F32 ? 4 : 2;
-        const char *row = h < hq ? static_cast<const char *>(a.q) + (t * a.ldq + (long)h * D) * es
-                        : h < hq + c.Hkv ? static_cast<const char *>(a.k) + (t * a.ldk + (long)(h - hq) * D) * es
-                                         : static_cast<const char *>(a.v) + (t * a.ldv + (long)(h - hq - c.Hkv) * D) * es;
-        // values, and elements the rotation leaves alone, go through the same two groups: a
-        // value row is read at the offsets of the rotation too (they cover the head all the same)
-        load4<ST>(row, e0, x[i][0]);
-        load4<ST>(row, e1, x[i][1]);
+        if (h0 + i * HPI < heads) {
+            load4<ST>(src, e0 + i * HPI * D, x[i][0]);
+            load4<ST>(src, e1 + i * HPI * D, x[i][1]);
+        }
     }
     // the token's sequence b, its tokens' first row and count, and its length: a lane looks at one sequence, all three
     // words at once, so that only the page table's word waits for another
@@ -158,26 +159,26 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
             sincospif((float)half_turns * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31
         }
     }
-    int page = -1;
-    if (place < (long)c.max_pages * c.page)
-        page = page_of(c, c.tables + (size_t)b * c.max_pages, (int)place);
-    else
-        set_dev_error(DEVERR_BAD_PAGE);
+    uint16_t *dst;
+    size_t step = (size_t)HPI * D;      // from one of the warp's heads to its next
+    if (what == 0) {
+        dst = a.q_out + ((size_t)t * a.H + h0) * D;
+    } else {
+        int page = -1;
+        if (place < (long)c.max_pages * c.page)
+            page = page_of(c, c.tables + (size_t)b * c.max_pages, (int)place);
+        else
+            set_dev_error(DEVERR_BAD_PAGE);
+        if (page < 0) return;
+        dst = (what == 1 ? c.k : c.v) + cache_row<D>(c, page, h0, (int)place);
+        step *= c.page;
+    }
 #pragma unroll
     for (int i = 0; i < APPEND_ITERS; ++i) {
-        const int h = h0 + i * HPI;
-        if (h >= heads) break;
-        uint16_t *dst;
-        if (h < hq) {
-            dst = a.q_out + ((size_t)t * a.H + h) * D;
-        } else {
-            if (page < 0) continue;
-            const bool key = h < hq + c.Hkv;
-            dst = (key ? c.k : c.v) + cache_row<D>(c, page, h - hq - (key ? 0 : c.Hkv), (int)place);
-        }
+        if (h0 + i * HPI >= heads) break;
         float(&u)[4] = x[i][0];
         float(&v)[4] = x[i][1];
-        if (turned && h < hq + c.Hkv) {
+        if (turned) {
             if (a.pairs_layout) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -197,8 +198,8 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
                 }
             }
         }
-        store4<XT>(dst + e0, u);
-        store4<XT>(dst + e1, v);
+        store4<XT>(dst + i * step + e0, u);
+        store4<XT>(dst + i * step + e1, v);
     }
 }
 

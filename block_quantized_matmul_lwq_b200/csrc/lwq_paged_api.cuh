@@ -78,21 +78,18 @@ int rope_check(const lwq_rope *r, int D) {
 }
 
 template <int ST, int XT>
-cudaError_t launch_append(int D, int iters, const AppendArgs &a, const lwq_rope &rope, unsigned blocks, cudaStream_t st) {
-    constexpr int N = APPEND_WARPS * 32;
+cudaError_t launch_append(int D, const AppendArgs &a, const lwq_rope &rope, unsigned blocks, cudaStream_t st) {
     if (D == 64)
-        iters == 8 ? kv_append_kernel<ST, XT, 64, 8><<<blocks, N, 0, st>>>(a, rope)
-                   : kv_append_kernel<ST, XT, 64, 4><<<blocks, N, 0, st>>>(a, rope);
+        kv_append_kernel<ST, XT, 64><<<blocks, APPEND_WARPS * 32, 0, st>>>(a, rope);
     else
-        iters == 8 ? kv_append_kernel<ST, XT, 128, 8><<<blocks, N, 0, st>>>(a, rope)
-                   : kv_append_kernel<ST, XT, 128, 4><<<blocks, N, 0, st>>>(a, rope);
+        kv_append_kernel<ST, XT, 128><<<blocks, APPEND_WARPS * 32, 0, st>>>(a, rope);
     return cudaGetLastError();
 }
 template <int ST>
-cudaError_t launch_append_xt(int dtype, int D, int iters, const AppendArgs &a, const lwq_rope &rope, unsigned blocks,
+cudaError_t launch_append_xt(int dtype, int D, const AppendArgs &a, const lwq_rope &rope, unsigned blocks,
                              cudaStream_t st) {
-    return dtype == LWQ_ACT_F16 ? launch_append<ST, X_F16>(D, iters, a, rope, blocks, st)
-                                : launch_append<ST, X_BF16>(D, iters, a, rope, blocks, st);
+    return dtype == LWQ_ACT_F16 ? launch_append<ST, X_F16>(D, a, rope, blocks, st)
+                                : launch_append<ST, X_BF16>(D, a, rope, blocks, st);
 }
 
 // The checks that both attention calls make, and the kernels' view of the arguments.
@@ -139,7 +136,11 @@ cudaError_t launch_paged_decode(const PagedPrefixArgs &k, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // behind a prefix's row tiles: a dependent launch that starts as their CTAs end and waits for the last of them at its own end
     if ((e = launch_k(kern, d.ctas, PD_WARPS * 32, smem, st, k.prefix != nullptr, d)) != cudaSuccess) return e;
-    if (!k.prefix) return launch_k(paged_combine_kernel<XT, D>, d.ctas * d.a.G, PC_THREADS, 0, st, true, d);
+    if (!k.prefix) {
+        const int parts = combine_parts((long)d.a.c.B * d.a.c.Hkv, d.a.G, d.ctas), n = d.a.G * D / parts;
+        const int threads = n >= PC_THREADS ? PC_THREADS : 2 * n <= PC_THREADS ? 2 * n : n;   // two groups where they fit
+        return launch_k(paged_combine_kernel<XT, D>, d.ctas * parts, threads, 0, st, true, d, parts);
+    }
     return launch_k(paged_prefix_combine_kernel<XT, D>, (int)(((long)d.a.c.B * d.a.H + 7) / 8), 256, 0, st, true, k);
 }
 template <int XT, int D, int PARTS>
@@ -327,13 +328,11 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
     a.positions = positions;
     a.T = T;
     a.H = H;
-    // rows of heads per warp: 8 when that still leaves the GPU a few thousand warps (a prompt), else 4
-    const int heads = (q ? H : 0) + 2 * cache->Hkv, wide = 8 * (256 / D);
-    const int iters = (double)T * ((heads + wide - 1) / wide) >= 4096.0 ? 8 : 4;
-    const int per = iters * (256 / D);          // heads per warp
-    a.units = (heads + per - 1) / per;
-    const double warps = (double)T * a.units;
-    if (warps > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
+    const int per = APPEND_ITERS * (256 / D);   // heads per warp
+    a.uq = q ? (H + per - 1) / per : 0;
+    a.uk = (cache->Hkv + per - 1) / per;
+    const int units = a.uq + 2 * a.uk;
+    if ((double)T * units > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
     a.rope = rope ? 1 : 0;
     a.pairs_layout = rope && rope->layout == LWQ_ROPE_PAIRS;
     lwq_rope r;
@@ -341,15 +340,15 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
         r = *rope;
     else
         memset(&r, 0, sizeof(r));
-    const unsigned blocks = (unsigned)(((long)T * a.units + APPEND_WARPS - 1) / APPEND_WARPS);
+    const unsigned blocks = (unsigned)(((long)T * units + APPEND_WARPS - 1) / APPEND_WARPS);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (src == LWQ_ACT_F32)
-        e = launch_append_xt<X_F32>(cache->dtype, D, iters, a, r, blocks, st);
+        e = launch_append_xt<X_F32>(cache->dtype, D, a, r, blocks, st);
     else if (src == LWQ_ACT_F16)
-        e = launch_append_xt<X_F16>(cache->dtype, D, iters, a, r, blocks, st);
+        e = launch_append_xt<X_F16>(cache->dtype, D, a, r, blocks, st);
     else
-        e = launch_append_xt<X_BF16>(cache->dtype, D, iters, a, r, blocks, st);
+        e = launch_append_xt<X_BF16>(cache->dtype, D, a, r, blocks, st);
     if (e != cudaSuccess) return LWQ_ERR_CUDA;
     t_last_launches = 1;
     return LWQ_OK;

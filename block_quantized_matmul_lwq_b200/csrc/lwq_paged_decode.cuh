@@ -390,49 +390,56 @@ __device__ __forceinline__ void store_out(const PagedAttnArgs &a, size_t at, flo
         static_cast<float *>(a.out)[at] = v;
 }
 
-// Merges the pairs that several CTAs worked on: a block per (CTA in whose run
-// a pair begins, query head), D columns by groups of threads that take every
-// so-manieth partial result.  The order of every addition is fixed by the
-// sizes.  Most blocks have nothing to do.
+// Merges the pairs that several CTAs worked on.  `parts` blocks per CTA in whose
+// run such a pair begins (most have none) share its G * D columns; a block's
+// threads take its columns in as many groups as fit, each group every so-manieth
+// partial result, eight loads in flight.  The order of every addition is fixed
+// by the sizes.  One block per CTA does for pairs cut in two or three (4.0 us
+// after the 125 us of 48 ragged sequences; a block per head 6.4 us, most of it
+// blocks that find nothing to do); a pair over 37 CTAs wants a block per head
+// (one sequence of 100003 tokens: 7 us, against 12 us).
 constexpr int PC_THREADS = 512;
+inline int combine_parts(long pairs, int G, int ctas) { return 4 * pairs <= ctas ? G : 1; }
 template <int XT, int D>
-__global__ void __launch_bounds__(PC_THREADS) paged_combine_kernel(const PagedDecodeArgs d) {
-    constexpr int NGR = PC_THREADS / D, PS = part_stride(D), U = 4;
-    __shared__ float gm[NGR], gl[NGR], go[NGR][D];
+__global__ void __launch_bounds__(PC_THREADS) paged_combine_kernel(const PagedDecodeArgs d, int parts) {
+    constexpr int PS = part_stride(D), U = 8;
+    __shared__ float gm[PC_THREADS], gl[PC_THREADS], go[PC_THREADS];
     const PagedAttnArgs &a = d.a;
-    const int i0 = blockIdx.x / a.G, h = blockIdx.x % a.G;
+    const int i0 = blockIdx.x / parts, n = a.G * D / parts, c0 = (blockIdx.x % parts) * n;   // columns [c0, c0 + n)
     pdl_wait();
     const int4 sp = __ldcg(d.splits + i0);
     if (sp.z == 0) return;
-    const int e = threadIdx.x % D, grp = threadIdx.x / D;
-    float M = -INFINITY, L = 0.f, A[1] = {0.f};
-    for (int s0 = grp; s0 < sp.z; s0 += NGR * U) {
-        float mv[U], lv[U], av[U][1];
+    const int groups = n < (int)blockDim.x ? (int)blockDim.x / n : 1, grp = groups > 1 ? threadIdx.x / n : 0;
+    for (int x = groups > 1 ? threadIdx.x % n : threadIdx.x; x < n; x += blockDim.x) {
+        const int col = c0 + x, h = col / D, e = col % D;
+        float M = -INFINITY, L = 0.f, A[1] = {0.f};
+        for (int s0 = grp; s0 < sp.z; s0 += groups * U) {
+            float mv[U], lv[U], av[U][1];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int s = s0 + u * NGR;
-            const float *p = d.slots + (((size_t)(i0 + (s < sp.z ? s : 0)) * 2 + (s == 0 ? sp.w : 0)) * a.G + h) * PS;
-            mv[u] = s < sp.z ? __ldcg(p) : -INFINITY;
-            lv[u] = __ldcg(p + 1);
-            av[u][0] = __ldcg(p + 4 + e);
+            for (int u = 0; u < U; ++u) {
+                const int s = s0 + u * groups < sp.z ? s0 + u * groups : 0;
+                const float *p = d.slots + (((size_t)(i0 + s) * 2 + (s == 0 ? sp.w : 0)) * a.G + h) * PS;
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p));
+                mv[u] = s0 + u * groups < sp.z ? ml.x : -INFINITY;
+                lv[u] = ml.y;
+                av[u][0] = __ldcg(p + 4 + e);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) merge_part(M, L, A, mv[u], lv[u], av[u]);
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) merge_part(M, L, A, mv[u], lv[u], av[u]);
+        if (groups > 1) {   // (blockDim.x is then a multiple of n: one round, every thread takes part)
+            gm[threadIdx.x] = M;
+            gl[threadIdx.x] = L;
+            go[threadIdx.x] = A[0];
+            __syncthreads();
+            if (grp > 0) return;
+            for (int i = 1; i < groups; ++i) {
+                const float v[1] = {go[i * n + x]};
+                merge_part(M, L, A, gm[i * n + x], gl[i * n + x], v);
+            }
+        }
+        store_out<XT>(a, ((size_t)sp.x * a.H + (size_t)sp.y * a.G) * D + col, A[0] / L);
     }
-    if (e == 0) {
-        gm[grp] = M;
-        gl[grp] = L;
-    }
-    go[grp][e] = A[0];
-    __syncthreads();
-    if (grp) return;
-    float Mt = -INFINITY, Lt = 0.f, At[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NGR; ++i) {
-        const float v[1] = {go[i][e]};
-        merge_part(Mt, Lt, At, gm[i], gl[i], v);
-    }
-    store_out<XT>(a, ((size_t)sp.x * a.H + (size_t)sp.y * a.G + h) * D + e, At[0] / Lt);
 }
 
 // Adds the prefix's partial results to each row's own: a warp per (sequence,
