@@ -36,8 +36,8 @@ namespace lwq {
 constexpr int TILE_ROWS = 128;
 constexpr int PAIR_ROWS = 2 * TILE_ROWS;
 constexpr int TILE_THREADS = 384;
-// registers per thread after the split: 128 x 88 + 256 x 208 = 64512, the 384 x 168 of the launch
-constexpr int TILE_REGS_FEED = 88, TILE_REGS_SOFTMAX = 208;
+// registers per thread after the split: 128 x 56 + 256 x 224 = 64512, the 384 x 168 of the launch
+constexpr int TILE_REGS_FEED = 56, TILE_REGS_SOFTMAX = 224;
 constexpr uint32_t TILE_TMEM_COLS = 512;
 constexpr float TILE_SLACK = 8.f;      // growth of a row's maximum that needs no rescaling
 
