@@ -226,7 +226,7 @@ struct RunScan {
     int lo, hi;
     long excl, mine, all;
     template <class W>
-    __device__ __forceinline__ RunScan(int count, long *scratch, W weight) {
+    __device__ __forceinline__ void build(int count, long *scratch, W weight) {
         const int per = (count + NT - 1) / NT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         lo = min(count, (int)threadIdx.x * per);
         hi = min(count, lo + per);
@@ -268,5 +268,33 @@ struct RunScan {
         *before = scratch[NT / 32 + 1];
     }
 };
+
+// The same by each warp for itself, 32 runs at a time, without a barrier: for
+// short lists (a block-wide scan's barriers cost more than up to four rounds).
+constexpr int WARP_RUNS = 128;
+// false: place `want` lies behind the last run
+template <class W>
+__device__ __forceinline__ bool warp_run_locate(int count, long want, int *run, long *before, W weight) {
+    const int lane = threadIdx.x & 31;
+    long base = 0;
+    for (int i0 = 0; i0 < count; i0 += 32) {
+        const long mine = i0 + lane < count ? weight(i0 + lane) : 0;
+        long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, want < base + incl);
+        if (hit) {
+            const int at = __ffs(hit) - 1;
+            *run = i0 + at;
+            *before = base + __shfl_sync(0xffffffffu, incl - mine, at);
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+}
 
 }  // namespace lwq

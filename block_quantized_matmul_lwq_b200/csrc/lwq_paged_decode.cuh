@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
 
     // this CTA's run of units, and the sequence that it begins in
     auto units = [&](int b) { return units_of(own_len(c, b)); };
-    RunScan<PD_WARPS * 32> scan(c.B, scratch, units);
+    RunScan<PD_WARPS * 32> scan;
+    scan.build(c.B, scratch, units);
     const long total = scan.all * c.Hkv;
     const Runs runs(total, d.ctas);
     const long u0 = runs.start(blockIdx.x), u1 = runs.start(blockIdx.x + 1);

@@ -192,17 +192,23 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         rs.len = 0;
         pl = pair;
     } else {
-        long *scratch = reinterpret_cast<long *>(sm);
-        if (threadIdx.x < c.B) asm volatile("prefetch.global.L1 [%0];" ::"l"(c.lens + threadIdx.x));
-        RunScan<TILE_THREADS> scan(c.B, scratch, [&](int b) { return pairs_of(token_count(a, b), a.G); });
-        if (pair >= scan.all) return;
+        auto weight = [&](int b) { return pairs_of(token_count(a, b), a.G); };
         long before;
-        scan.locate(pair, scratch, &rs.b, &before, [&](int b) { return pairs_of(token_count(a, b), a.G); });
+        if (threadIdx.x < c.B) asm volatile("prefetch.global.L1 [%0];" ::"l"(c.lens + threadIdx.x));
+        if (c.B <= WARP_RUNS) {
+            if (!warp_run_locate(c.B, pair, &rs.b, &before, weight)) return;
+        } else {
+            long *scratch = reinterpret_cast<long *>(sm);
+            RunScan<TILE_THREADS> scan;
+            scan.build(c.B, scratch, weight);
+            if (pair >= scan.all) return;
+            scan.locate(pair, scratch, &rs.b, &before, weight);
+            __syncthreads();   // the scratch is shared memory of the tiles
+        }
         rs.tok0 = first_token(a, rs.b);
         rs.n = token_count(a, rs.b);
         rs.len = __ldg(c.lens + rs.b);
         pl = pairs_of(rs.n, a.G) - 1 - (pair - before);   // the rows that see most first
-        __syncthreads();                                   // the scratch is shared memory of the tiles
     }
     rs.row0 = (int)(pl * PAIR_ROWS);
     const int rows = min(rs.n * a.G - rs.row0, PAIR_ROWS);   // live rows of the pair
