@@ -47,10 +47,11 @@ __device__ __forceinline__ size_t cache_row(const PagedArgs &c, int p, int g, in
 // A group of D / 8 lanes takes one head of a token: 4 pairs per lane, i.e. 4 + 4
 // (HALF) or 8 (PAIRS) consecutive elements, so that each warp-wide access is
 // whole 128-byte lines; a warp takes 4 such accesses of one token's queries,
-// keys or values with all their loads in flight before the first store, and its
-// lanes' four (cos, sin) are computed once for all of them.  So a single token
-// is spread over several warps (40 rotated and 8 other heads of 128: 6 warps),
-// and no warp decides anything per head.
+// keys or values with all their loads in flight before the first store, and no
+// warp decides anything per head.  A block is one token's warps (up to 8: 40
+// rotated and 8 other heads of 128 take 6), which share the (cos, sin) of the
+// token's pairs: computed per warp they were half of all instructions (7776
+// tokens, 48 heads of 128: 58.5 us, and 51 us shared: 5.6 TB/s).
 //
 // The angle position * f is kept in turns as a 64-bit fraction: the low 64 bits
 // of position * turn are the exact product modulo one turn, and their top 32
@@ -58,7 +59,7 @@ __device__ __forceinline__ size_t cache_row(const PagedArgs &c, int p, int g, in
 // 2^31 costs no accuracy (fp32 angles would be off by whole turns there), and
 // no 64-bit floating point is used.
 constexpr int APPEND_ITERS = 4;
-constexpr int APPEND_WARPS = 4;
+constexpr int APPEND_WARPS = 8;   // at most
 
 struct AppendArgs {
     PagedArgs c;
@@ -98,11 +99,10 @@ template <int ST, int XT, int D>
 __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const AppendArgs a, const lwq_rope rope) {
     constexpr int LPH = D / 8;          // lanes per head
     constexpr int HPI = 32 / LPH;       // heads per warp access
-    const int lane = threadIdx.x & 31;
-    const long w = (long)blockIdx.x * APPEND_WARPS + (threadIdx.x >> 5);
-    const int units = a.uq + 2 * a.uk, t = (int)(w / units);
-    int unit = (int)(w % units);
-    if (t >= a.T) return;
+    __shared__ float2 trig[64];         // (cos, sin) of the token's pairs
+    const int lane = threadIdx.x & 31, t = blockIdx.x;
+    int unit = blockIdx.y * APPEND_WARPS + (threadIdx.x >> 5);
+    const bool idle = unit >= a.uq + 2 * a.uk;   // (the last block of a token's)
     const PagedArgs &c = a.c;
     const int what = unit < a.uq ? 0 : unit < a.uq + a.uk ? 1 : 2;   // q, k, v
     unit -= what == 0 ? 0 : what == 1 ? a.uq : a.uq + a.uk;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
     float x[APPEND_ITERS][2][4];
 #pragma unroll
     for (int i = 0; i < APPEND_ITERS; ++i) {
-        if (h0 + i * HPI < heads) {
+        if (!idle && h0 + i * HPI < heads) {
             load4<ST>(src, e0 + i * HPI * D, x[i][0]);
             load4<ST>(src, e1 + i * HPI * D, x[i][1]);
         }
@@ -148,16 +148,25 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32) kv_append_kernel(const Appe
     }
     const long place = (long)len - n + idx;
     if (place < 0) return;              // padding
-    float cs[4], sn[4];
-    if (turned) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = a.positions ? __ldg(a.positions + (size_t)rope.axis[4 * pi + i] * a.T + t)
+    if (a.rope) {
+        if ((int)threadIdx.x < rope.rot_dim / 2) {
+            const int p = a.positions ? __ldg(a.positions + (size_t)rope.axis[threadIdx.x] * a.T + t)
                                       : c.prefix_len + (int)place;
-            const uint64_t turns = (uint64_t)(int64_t)p * rope.turn[4 * pi + i];
+            const uint64_t turns = (uint64_t)(int64_t)p * rope.turn[threadIdx.x];
             const int half_turns = (int)(uint32_t)((turns + 0x80000000ull) >> 32);
-            sincospif((float)half_turns * 4.656612873077393e-10f, &sn[i], &cs[i]);   // 2^-31
+            float sn, cs;
+            sincospif((float)half_turns * 4.656612873077393e-10f, &sn, &cs);   // 2^-31
+            trig[threadIdx.x] = make_float2(cs, sn);
         }
+        __syncthreads();   // (the block is one token's: all of it left above, or none)
+    }
+    if (idle) return;
+    float cs[4], sn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = turned ? trig[4 * pi + i] : make_float2(1.f, 0.f);
+        cs[i] = v.x;
+        sn[i] = v.y;
     }
     uint16_t *dst;
     size_t step = (size_t)HPI * D;      // from one of the warp's heads to its next
@@ -223,8 +232,8 @@ __host__ __device__ constexpr int part_stride(int D) { return D + 4; }
 // memory, free for other use after a barrier behind the last call.
 template <int NT>
 struct RunScan {
-    int lo, hi;
-    long excl, mine, all;
+    int lo = 0, hi = 0;
+    long excl = 0, mine = 0, all = 0;
     template <class W>
     __device__ __forceinline__ void build(int count, long *scratch, W weight) {
         const int per = (count + NT - 1) / NT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -78,18 +78,21 @@ int rope_check(const lwq_rope *r, int D) {
 }
 
 template <int ST, int XT>
-cudaError_t launch_append(int D, const AppendArgs &a, const lwq_rope &rope, unsigned blocks, cudaStream_t st) {
+cudaError_t launch_append(int D, const AppendArgs &a, const lwq_rope &rope, cudaStream_t st) {
+    // a block per token (several where its rows need more than 8 warps): never less than the 64 threads of its pairs,
+    // as k and v take a warp each
+    const int units = a.uq + 2 * a.uk, warps = units < APPEND_WARPS ? units : APPEND_WARPS;
+    const dim3 grid((unsigned)a.T, (unsigned)((units + APPEND_WARPS - 1) / APPEND_WARPS));
     if (D == 64)
-        kv_append_kernel<ST, XT, 64><<<blocks, APPEND_WARPS * 32, 0, st>>>(a, rope);
+        kv_append_kernel<ST, XT, 64><<<grid, warps * 32, 0, st>>>(a, rope);
     else
-        kv_append_kernel<ST, XT, 128><<<blocks, APPEND_WARPS * 32, 0, st>>>(a, rope);
+        kv_append_kernel<ST, XT, 128><<<grid, warps * 32, 0, st>>>(a, rope);
     return cudaGetLastError();
 }
 template <int ST>
-cudaError_t launch_append_xt(int dtype, int D, const AppendArgs &a, const lwq_rope &rope, unsigned blocks,
-                             cudaStream_t st) {
-    return dtype == LWQ_ACT_F16 ? launch_append<ST, X_F16>(D, a, rope, blocks, st)
-                                : launch_append<ST, X_BF16>(D, a, rope, blocks, st);
+cudaError_t launch_append_xt(int dtype, int D, const AppendArgs &a, const lwq_rope &rope, cudaStream_t st) {
+    return dtype == LWQ_ACT_F16 ? launch_append<ST, X_F16>(D, a, rope, st)
+                                : launch_append<ST, X_BF16>(D, a, rope, st);
 }
 
 // The checks that both attention calls make, and the kernels' view of the arguments.
@@ -331,8 +334,7 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
     const int per = APPEND_ITERS * (256 / D);   // heads per warp
     a.uq = q ? (H + per - 1) / per : 0;
     a.uk = (cache->Hkv + per - 1) / per;
-    const int units = a.uq + 2 * a.uk;
-    if ((double)T * units > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
+    if ((a.uq + 2 * a.uk) / APPEND_WARPS >= 65535) return LWQ_ERR_UNSUPPORTED;
     a.rope = rope ? 1 : 0;
     a.pairs_layout = rope && rope->layout == LWQ_ROPE_PAIRS;
     lwq_rope r;
@@ -340,15 +342,14 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
         r = *rope;
     else
         memset(&r, 0, sizeof(r));
-    const unsigned blocks = (unsigned)(((long)T * units + APPEND_WARPS - 1) / APPEND_WARPS);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (src == LWQ_ACT_F32)
-        e = launch_append_xt<X_F32>(cache->dtype, D, a, r, blocks, st);
+        e = launch_append_xt<X_F32>(cache->dtype, D, a, r, st);
     else if (src == LWQ_ACT_F16)
-        e = launch_append_xt<X_F16>(cache->dtype, D, a, r, blocks, st);
+        e = launch_append_xt<X_F16>(cache->dtype, D, a, r, st);
     else
-        e = launch_append_xt<X_BF16>(cache->dtype, D, a, r, blocks, st);
+        e = launch_append_xt<X_BF16>(cache->dtype, D, a, r, st);
     if (e != cudaSuccess) return LWQ_ERR_CUDA;
     t_last_launches = 1;
     return LWQ_OK;
