@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblwq.so")
@@ -75,10 +76,13 @@ class lwq_paged(ctypes.Structure):
 
     def __init__(self, act: int, k, v, tables, lens, *, B: int, Hkv: int, D: int, page: int, max_pages: int,
                  num_pages: int, prefix=None, prefix_len: int = 0):
-        super().__init__(_ptr(k), _ptr(v), _ptr(tables), _ptr(lens), _ptr(prefix), prefix_len, act, B, Hkv, D, page,
-                         max_pages, num_pages)
+        n = num_pages * Hkv * page * D
+        super().__init__(_tensor(k, "k", 2, n), _tensor(v, "v", 2, n), _tensor(tables, "tables", 4, B * max_pages),
+                         _tensor(lens, "lens", 4, B), _tensor(prefix, "prefix", 4, -(-prefix_len // max(page, 1))),
+                         prefix_len, act, B, Hkv, D, page, max_pages, num_pages)
         self.owners = (k, v, tables, lens, prefix)
-        self.at = ctypes.addressof(self)
+
+    at = property(ctypes.addressof)
 
 
 class lwq_rope(ctypes.Structure):
@@ -87,9 +91,7 @@ class lwq_rope(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("axes", ctypes.c_int),
                 ("reserved", ctypes.c_int), ("turn", ctypes.c_uint64 * 64), ("axis", ctypes.c_uint8 * 64)]
 
-    def __init__(self):
-        super().__init__()
-        self.at = ctypes.addressof(self)
+    at = property(ctypes.addressof)
 
 
 def _load() -> ctypes.CDLL:
@@ -159,6 +161,19 @@ def _ptr(p) -> int:
         return 0
     if isinstance(p, int):
         return p
+    return int(p.data_ptr())
+
+
+def _tensor(p, name: str, size: int, count: int, dense: bool = True) -> int:
+    """_ptr of a tensor that a kernel will index: refused where it lies on the host or on another device than the
+    current one, holds elements of another size than the call's, is too small or (dense) not contiguous."""
+    if p is None or isinstance(p, int) or not hasattr(p, "element_size"):
+        return _ptr(p)
+    if not p.is_cuda or p.get_device() != sys.modules["torch"].cuda.current_device():
+        raise ValueError(f"{name}: a tensor on the current CUDA device is needed, not on {p.device}")
+    if p.element_size() != size or (dense and (p.numel() < count or not p.is_contiguous())):
+        raise ValueError(f"{name}: {count} contiguous elements of {size} bytes are needed, not {tuple(p.shape)} of "
+                         f"{p.dtype} with strides {p.stride()}")
     return int(p.data_ptr())
 
 
@@ -267,8 +282,12 @@ def lwq_rope_init(rot_dim: int, base: float = 10000.0, layout: int = LWQ_ROPE_HA
 def lwq_kv_append(cache: lwq_paged, rope, src: int, q, ldq: int, k, ldk: int, v, ldv: int, q_out, T: int, H: int,
                   cu_tokens=None, positions=None, stream=None) -> None:
     """Rotate q and k by position (rope None: not) and store k and v in the cache (see include/lwq.h)."""
-    _check(_lib.lwq_kv_append(cache.at, None if rope is None else rope.at, src, _ptr(q), ldq,
-                              _ptr(k), ldk, _ptr(v), ldv, _ptr(q_out), _ptr(cu_tokens), _ptr(positions), T, H,
+    es = 4 if src == LWQ_ACT_F32 else 2
+    _check(_lib.lwq_kv_append(cache.at, None if rope is None else rope.at, src, _tensor(q, "q", es, 0, False), ldq,
+                              _tensor(k, "k", es, 0, False), ldk, _tensor(v, "v", es, 0, False), ldv,
+                              _tensor(q_out, "q_out", 2, T * H * cache.D),
+                              _tensor(cu_tokens, "cu_tokens", 4, cache.B + 1),
+                              _tensor(positions, "positions", 4, T * (1 if rope is None else rope.axes)), T, H,
                               _stream(stream)), "lwq_kv_append")
 
 
@@ -278,7 +297,9 @@ def lwq_attention_paged_workspace_size(cache: lwq_paged, H: int) -> int:
 
 def lwq_attention_paged(cache: lwq_paged, q, out, H: int, scale: float, flags: int = 0, stream=None) -> None:
     """Decode attention, one query token per sequence, over the paged cache and its shared prefix."""
-    _check(_lib.lwq_attention_paged(cache.at, flags, _ptr(q), _ptr(out), H, float(scale),
+    n = cache.B * H * cache.D
+    _check(_lib.lwq_attention_paged(cache.at, flags, _tensor(q, "q", 2, n),
+                                    _tensor(out, "out", 2 if flags & LWQ_FLAG_OUT16 else 4, n), H, float(scale),
                                     _stream(stream)), "lwq_attention_paged")
 
 
@@ -289,5 +310,8 @@ def lwq_attention_prefill_workspace_size(cache: lwq_paged, T: int, H: int) -> in
 def lwq_attention_prefill(cache: lwq_paged, q, out, cu_tokens, T: int, H: int, scale: float, flags: int = 0,
                           stream=None) -> None:
     """Causal attention of the batch's new tokens over the cache that already holds them."""
-    _check(_lib.lwq_attention_prefill(cache.at, flags, _ptr(q), _ptr(out), _ptr(cu_tokens), T, H,
-                                      float(scale), _stream(stream)), "lwq_attention_prefill")
+    n = T * H * cache.D
+    _check(_lib.lwq_attention_prefill(cache.at, flags, _tensor(q, "q", 2, n),
+                                      _tensor(out, "out", 2 if flags & LWQ_FLAG_OUT16 else 4, n),
+                                      _tensor(cu_tokens, "cu_tokens", 4, cache.B + 1), T, H, float(scale),
+                                      _stream(stream)), "lwq_attention_prefill")

@@ -115,6 +115,9 @@ int paged_attn_args(const lwq_paged *c, int flags, const void *q, void *out, con
     a->causal = causal;
     a->out16 = (flags & LWQ_FLAG_OUT16) ? 1 : 0;
     a->qscale = scale * 1.4426950408889634f;   // log2(e): the kernels take exponentials as exp2
+    if (!isfinite(a->qscale)) return LWQ_ERR_INVALID_ARG;
+    const size_t n = (size_t)T * H * c->D;
+    if (overlap(q, 2 * n, out, (a->out16 ? 2 : 4) * n)) return LWQ_ERR_INVALID_ARG;
     return LWQ_OK;
 }
 

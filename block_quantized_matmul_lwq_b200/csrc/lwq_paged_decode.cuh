@@ -246,12 +246,12 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
                 float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[gg], mx);      // finite: key j0 is live
-                corr[gg] = exp2f(m[gg] - mn);           // 0 on the first step (m = -inf)
+                const float mn = fmaxf(m[gg], mx), base = mn == -INFINITY ? 0.f : mn;   // (scores may be -inf)
+                corr[gg] = exp2f(m[gg] - base);         // 0 on the first step (m = -inf)
                 float ps = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[e] = exp2f(p[e] - mn);            // 0 for a key past the end
+                    p[e] = exp2f(p[e] - base);          // 0 for a key past the end
                     ps += p[e];
                 }
                 l[gg] = fmaf(l[gg], corr[gg], ps);
@@ -333,10 +333,11 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
                 float M = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < PD_WARPS; ++w) M = fmaxf(M, sm_m[w][h]);
-                float L = 0.f, A = 0.f;   // M is finite: the first warp's first key is live
+                const float base = M == -INFINITY ? 0.f : M;
+                float L = 0.f, A = 0.f;
 #pragma unroll
                 for (int w = 0; w < PD_WARPS; ++w) {
-                    const float f = exp2f(sm_m[w][h] - M);
+                    const float f = exp2f(sm_m[w][h] - base);
                     L = fmaf(sm_l[w][h], f, L);
                     A = fmaf(sm_o[w][h][e], f, A);
                 }

@@ -660,7 +660,10 @@ __global__ void __launch_bounds__(256) paged_tile_combine_kernel(const PagedTile
     const int lane = threadIdx.x & 31;
     const long w = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int t = (int)(w / a.H), hh = (int)(w % a.H), g = hh / a.G;
-    if (t >= a.T) return;
+    if (t >= a.T) {
+        pdl_wait();
+        return;
+    }
     // the token's sequence, and the pairs of row tiles before it
     int b = 0, tok0 = 0, n = 0;
     long before = 0;
@@ -680,7 +683,10 @@ __global__ void __launch_bounds__(256) paged_tile_combine_kernel(const PagedTile
             break;
         }
     }
-    if (n == 0) return;   // behind the last sequence
+    if (n == 0) {   // behind the last sequence (the wait all the same: this kernel may not end before the tiles')
+        pdl_wait();
+        return;
+    }
     const long ri = (long)(t - tok0) * a.G + hh % a.G;
     const long pair = before + pairs_of(n, a.G) - 1 - ri / PAIR_ROWS;
     const int r = (int)(ri % PAIR_ROWS);

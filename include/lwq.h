@@ -317,7 +317,8 @@ int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const do
  *              [T][(H + 2 Hkv) D]: q = y, k = y + H D, v = y + (H + Hkv) D,
  *              all three strides (H + 2 Hkv) D.)
  *   q_out      [T][H][D] in the cache's dtype; may not overlap the inputs.
- *              q and q_out may both be NULL: keys and values only.
+ *              q and q_out may both be NULL: keys and values only (H is
+ *              checked all the same).
  *   cu_tokens  [B + 1] int32, device, ascending from 0: sequence b's tokens
  *              are cu_tokens[b] .. cu_tokens[b + 1] - 1, the last ones of its
  *              lens[b] tokens.  NULL: one token per sequence (T == B).
@@ -328,7 +329,8 @@ int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const do
  * tokens whose place in the cache would be negative (lens[b] 0), are padding:
  * nothing is written for them.  A place beyond max_pages * page is
  * reported as LWQ_ERR_BAD_PAGE and its k and v are dropped.  Two tokens of a
- * call may not share a place in the cache.  One kernel, no workspace.
+ * call may not share a place in the cache (which of them stays would be open).
+ * One kernel, no workspace.
  * Errors: LWQ_ERR_INVALID_ARG (sizes, NULL pointers, T != B without
  * cu_tokens, a stride below its row, q_out over an input), LWQ_ERR_UNSUPPORTED
  * (types, D, page, H / Hkv > 16, rot_dim > D, sizes past 31 bits),
@@ -350,10 +352,12 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
  * are read once for the whole batch, as one matrix product over all B queries.
  * Needs the workspace of lwq_init: lwq_attention_paged_workspace_size bytes,
  * which depends on the sizes in *cache (its pointers are not read) and never
- * on the sequences' lengths.  lwq_attention_paged_workspace_size returns 0
- * for invalid sizes.  Errors as lwq_kv_append's, LWQ_ERR_INVALID_ARG for a
- * scale that is not finite, LWQ_ERR_NOT_INITIALIZED and
- * LWQ_ERR_WORKSPACE_TOO_SMALL. */
+ * on the sequences' lengths; like lwq_matmul's, calls sharing it must be
+ * ordered (one stream, or events).  lwq_attention_paged_workspace_size returns
+ * 0 for invalid sizes.  The keys and values of live tokens must be finite.
+ * Errors as lwq_kv_append's, LWQ_ERR_INVALID_ARG for a scale that is not finite
+ * and for an out that overlaps q (there is no in-place form),
+ * LWQ_ERR_NOT_INITIALIZED and LWQ_ERR_WORKSPACE_TOO_SMALL. */
 size_t lwq_attention_paged_workspace_size(const lwq_paged *cache, int H);
 int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *out, int H, float scale,
                         void *stream);
@@ -364,8 +368,8 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
  * each, T == B).  The token at place j of its sequence (0 .. lens[b] - 1)
  * sees the prefix and the tokens 0 .. j.  A token that sees nothing gets
  * zeros; rows from cu_tokens[B] on are left as they were.  The values of the
- * sequence's own tokens must be finite: a token's probability of 0 for a
- * later one multiplies its value.  Workspace and errors as
+ * sequence's later tokens must be finite too: a token's probability of 0 for
+ * them multiplies their values.  Workspace and errors as
  * lwq_attention_paged; it is needed only when few tokens meet long caches
  * and the keys are split. */
 size_t lwq_attention_prefill_workspace_size(const lwq_paged *cache, int T, int H);
@@ -393,8 +397,8 @@ int lwq_get_device_error(void);
  * lwq_get_device_error.  Faults nothing and hangs nothing. */
 int lwq_selftest_timeout(unsigned timeout_us, void *stream);
 
-/* Number of kernels the last successful lwq_matmul / lwq_matmul_config call
- * on this thread enqueued. */
+/* Number of kernels the last successful lwq_matmul, lwq_matmul_config,
+ * lwq_kv_append or attention call on this thread enqueued. */
 int lwq_last_launch_count(void);
 
 /* Library version, e.g. 0x000100 for 0.1.0. */

@@ -402,8 +402,27 @@ def test_prefill_without_offsets_is_decode(dev):
     assert_attention(p, out, True)
 
 
-def test_prefill_many_short_sequences(dev):
-    new = [1 + (5 * b) % 7 for b in range(90)]
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("ramp", [False, True])
+def test_prefill_sums_kept_past_1024_keys(dev, dtype, ramp):
+    """fp32 results over more keys than the accumulator sums at a time, whole (160 row tiles: no split) and split;
+    with scores that grow, so that the kept sums have to be rescaled."""
+    p = Problem(dev, dtype, [2400], 20, 20, 64, 64, new=[1800], seed=6)
+    long = Problem(dev, dtype, [40000], 8, 8, 64, 256, new=[64], seed=7)
+    if ramp:
+        for q in (p, long):
+            n = q.lens[0]
+            j = torch.arange(n)
+            up = (torch.arange(n) * (6.0 / n)).to(TYPES[dtype]).to(dev)
+            q.kc[q.tables_h[0][j // q.page].long().to(dev), :, (j % q.page).to(dev), :4] = up[:, None, None]
+            q.q[..., :4] = 4.0
+    check_attention(p, causal=True)
+    check_attention(long, causal=True)
+
+
+@pytest.mark.parametrize("B", [90, 200])
+def test_prefill_many_short_sequences(dev, B):
+    new = [1 + (5 * b) % 7 for b in range(B)]
     lens = [n + (11 * b) % 60 for b, n in enumerate(new)]
     check_attention(Problem(dev, "f16", lens, 8, 4, 64, 16, new=new, seed=5), causal=True)
 
@@ -475,6 +494,66 @@ def test_workspace_is_checked(dev):
     finally:
         torch.cuda.synchronize(dev)
         lwq.lwq_init(_ARENA[0], WS_BYTES)
+
+
+def test_tensors_that_do_not_fit_are_refused(dev):
+    """int64 lengths, a strided query, an output of the other type or too small: refused before any launch."""
+    p = Problem(dev, "f16", [30, 5], 4, 2, 64, 16, seed=1)
+    f16, f32 = torch.zeros((2, 4, 64), dtype=torch.float16, device=dev), torch.zeros((2, 4, 64), device=dev)
+    p.lens_d = p.lens_d.long()
+    with pytest.raises(ValueError):
+        p.cache()
+    p.lens_d = p.lens_d.int()
+    cache = p.cache()
+    with pytest.raises(ValueError):
+        lwq.lwq_attention_paged(cache, p.q, f16, 4, p.scale)
+    with pytest.raises(ValueError):
+        lwq.lwq_attention_paged(cache, p.q, f32, 4, p.scale, flags=lwq.LWQ_FLAG_OUT16)
+    with pytest.raises(ValueError):
+        lwq.lwq_attention_paged(cache, p.q, f32[:1], 4, p.scale)
+    with pytest.raises(ValueError):
+        lwq.lwq_attention_paged(cache, p.q.transpose(0, 1), f32, 4, p.scale)
+    with pytest.raises(ValueError):
+        lwq.lwq_kv_append(cache, None, lwq.LWQ_ACT_F32, f16, 512, f16, 512, f16, 512, f16, 2, 4)
+    with pytest.raises(lwq.LwqError) as e:
+        lwq.lwq_attention_paged(cache, p.q, p.q, 4, p.scale, flags=lwq.LWQ_FLAG_OUT16)
+    assert e.value.status == lwq.LWQ_ERR_INVALID_ARG
+
+
+def test_two_captured_graphs_in_turn(dev):
+    """Two batches' decode steps, captured apart, share the workspace: replayed one after the other on one stream."""
+    ps = [Problem(dev, "f16", [700, 3, 0], 8, 2, 64, 16, prefix=90, seed=1), Problem(dev, "f16", [4000], 8, 2, 64, 32, seed=2)]
+    s = torch.cuda.Stream(dev)
+    outs, graphs = [torch.zeros((p.B, 8, 64), device=dev) for p in ps], []
+    for p, out in zip(ps, outs):
+        cache = p.cache()
+        lwq.lwq_attention_paged(cache, p.q, out, 8, p.scale, stream=s)
+        s.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            lwq.lwq_attention_paged(cache, p.q, out, 8, p.scale, stream=s)
+        out.zero_()
+    torch.cuda.synchronize(dev)
+    with torch.cuda.stream(s):
+        for _ in range(3):
+            for g in graphs:
+                g.replay()
+    torch.cuda.synchronize(dev)
+    for p, out in zip(ps, outs):
+        assert_attention(p, out, False)
+    graphs.clear()
+
+
+def test_prefill_no_live_token(dev):
+    """Every sequence of a captured batch without a new token, keys split or not: nothing is written."""
+    p = Problem(dev, "f16", [4000, 900], 8, 2, 64, 16, new=[0, 0], seed=1)
+    for T in (1, 3000):
+        out = torch.full((T, 8, 64), 5.0, device=dev)
+        q = torch.zeros((T, 8, 64), dtype=torch.float16, device=dev)
+        lwq.lwq_attention_prefill(p.cache(), q, out, p.cu_d, T, 8, p.scale)
+        torch.cuda.synchronize(dev)
+        assert (out == 5.0).all()
+    assert lwq.lwq_get_device_error() == lwq.LWQ_OK
 
 
 # ------------------------------------------------------------ a run of them all

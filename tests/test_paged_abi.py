@@ -74,6 +74,42 @@ def test_bad_attention_arguments(args, code):
                   flags=a["flags"]) == code
 
 
+def test_out_may_not_overlap_q():
+    """No in-place form, whichever type out has: q is read by CTAs that others do not wait for."""
+    n = 2 * 4 * 64                                      # B x H x D
+    for flags, es in ((0, 4), (lwq.LWQ_FLAG_OUT16, 2)):
+        for out in (FAKE, FAKE + 2 * n - 16, FAKE - es * n + 16):
+            assert status(lwq.lwq_attention_paged, cache(), FAKE, out, 4, 0.1, flags=flags) == lwq.LWQ_ERR_INVALID_ARG
+            assert status(lwq.lwq_attention_prefill, cache(), FAKE, out, None, 2, 4, 0.1,
+                          flags=flags) == lwq.LWQ_ERR_INVALID_ARG
+
+
+def test_scale_past_the_range_of_the_exponents():
+    """scale log2(e) has to be finite, as the kernels take powers of two."""
+    assert status(lwq.lwq_attention_paged, cache(), FAKE, QOUT, 4, 3e38) == lwq.LWQ_ERR_INVALID_ARG
+
+
+def test_tensors_on_the_host_are_refused():
+    torch = pytest.importorskip("torch")
+    t32, t16 = torch.zeros(4096), torch.zeros(4096, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        cache(k=t16)
+    with pytest.raises(ValueError):
+        cache(lens=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        lwq.lwq_attention_paged(cache(), t16, QOUT, 4, 0.1)
+    with pytest.raises(ValueError):
+        lwq.lwq_attention_prefill(cache(), FAKE, t32, FAKE, 2, 4, 0.1)
+    with pytest.raises(ValueError):
+        lwq.lwq_kv_append(cache(), None, lwq.LWQ_ACT_F32, FAKE, 512, t32, 512, FAKE, 512, QOUT, 2, 4)
+
+
+def test_a_copied_rotation_is_the_rotation():
+    rope = lwq.lwq_rope.from_buffer_copy(lwq.lwq_rope_init(128))
+    assert status(lwq.lwq_kv_append, cache(), rope, lwq.LWQ_ACT_F16, FAKE, 512, FAKE, 512, FAKE, 512, QOUT, 2,
+                  4) == lwq.LWQ_ERR_UNSUPPORTED        # looked at: wider than the head
+
+
 def test_prefill_counts():
     assert status(lwq.lwq_attention_prefill, cache(), FAKE, FAKE, FAKE, 0, 4, 0.1) == lwq.LWQ_ERR_INVALID_ARG
     assert status(lwq.lwq_attention_prefill, cache(), FAKE, FAKE, None, 3, 4, 0.1) == lwq.LWQ_ERR_INVALID_ARG
