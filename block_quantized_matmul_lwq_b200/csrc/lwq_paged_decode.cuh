@@ -84,7 +84,10 @@ struct PagedDecodeSmem {
     static constexpr int STAGES = D == 64 ? (NG == 2 ? 4 : 6) : (NG == 2 ? 2 : 3);
     static constexpr uint32_t ROWB = 2 * D, TILEB = 16 * ROWB, STAGEB = 2 * TILEB;
     static constexpr size_t RING = (size_t)PD_WARPS * STAGES * STAGEB;
-    static constexpr size_t MERGE = (size_t)PD_WARPS * 8 * NG * (D + 2) * 4;
+    // rows of the merge are 4 words apart in banks (8 heads at one bank each would make every store eight turns); two
+    // CTAs of the largest form still fit an SM's 228 KB
+    static constexpr int MROW = D + 4;
+    static constexpr size_t MERGE = (size_t)PD_WARPS * 8 * NG * (MROW + 2) * 4;
     static constexpr size_t TOTAL = RING + MERGE + 64;   // and the scan's words
 };
 
@@ -174,7 +177,8 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
 
     float(*sm_m)[8 * NG] = reinterpret_cast<float(*)[8 * NG]>(dsm + SM::RING);
     float(*sm_l)[8 * NG] = sm_m + PD_WARPS;
-    float(*sm_o)[8 * NG][D] = reinterpret_cast<float(*)[8 * NG][D]>(dsm + SM::RING + 2 * PD_WARPS * 8 * NG * 4);
+    float(*sm_o)[8 * NG][SM::MROW] =
+        reinterpret_cast<float(*)[8 * NG][SM::MROW]>(dsm + SM::RING + 2 * PD_WARPS * 8 * NG * 4);
 
     uint32_t qa[D / 16][2 * NG];
     float o[NG][D / 8][4], m[NG], l[NG];
@@ -320,10 +324,10 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
                     sm_l[warp][h] = ls;
                 }
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n) {   // hi rows + lo rows
-                    sm_o[warp][h][8 * n + 2 * t] = o[gg][n][0] + o[gg][n][2];
-                    sm_o[warp][h][8 * n + 2 * t + 1] = o[gg][n][1] + o[gg][n][3];
-                }
+                for (int n = 0; n < D / 8; ++n)   // hi rows + lo rows
+                    if (h < G)
+                        *reinterpret_cast<float2 *>(&sm_o[warp][h][8 * n + 2 * t]) =
+                            make_float2(o[gg][n][0] + o[gg][n][2], o[gg][n][1] + o[gg][n][3]);
             }
             __syncthreads();
             // a pair that this run began and finished is complete; any other is a part of one
