@@ -81,6 +81,10 @@ class lwq_paged(ctypes.Structure):
                          _tensor(lens, "lens", 4, B), _tensor(prefix, "prefix", 4, -(-prefix_len // max(page, 1))),
                          prefix_len, act, B, Hkv, D, page, max_pages, num_pages)
         self.owners = (k, v, tables, lens, prefix)
+        on = {p.get_device() for p in self.owners if hasattr(p, "get_device")}
+        if len(on) > 1:
+            raise ValueError(f"the cache's tensors are on several devices: {sorted(on)}")
+        self.device = on.pop() if on else None
 
     at = property(ctypes.addressof)
 
@@ -164,17 +168,27 @@ def _ptr(p) -> int:
     return int(p.data_ptr())
 
 
-def _tensor(p, name: str, size: int, count: int, dense: bool = True) -> int:
-    """_ptr of a tensor that a kernel will index: refused where it lies on the host or on another device than the
-    current one, holds elements of another size than the call's, is too small or (dense) not contiguous."""
-    if p is None or isinstance(p, int) or not hasattr(p, "element_size"):
+def _tensor(p, name: str, size: int, count: int = 0) -> int:
+    """_ptr of a tensor that a kernel will index: refused where it is on the host, holds elements of another size than
+    the call's, or, given a count, has fewer of them or is not contiguous."""
+    if p is None or p.__class__ is int:
+        return p or 0
+    try:
+        ok = p.is_cuda and p.element_size() == size and (not count or (p.numel() >= count and p.is_contiguous()))
+    except AttributeError:      # a pointer of another kind
         return _ptr(p)
-    if not p.is_cuda or p.get_device() != sys.modules["torch"].cuda.current_device():
-        raise ValueError(f"{name}: a tensor on the current CUDA device is needed, not on {p.device}")
-    if p.element_size() != size or (dense and (p.numel() < count or not p.is_contiguous())):
-        raise ValueError(f"{name}: {count} contiguous elements of {size} bytes are needed, not {tuple(p.shape)} of "
-                         f"{p.dtype} with strides {p.stride()}")
-    return int(p.data_ptr())
+    if not ok:
+        raise ValueError(f"{name}: {count or ''} elements of {size} bytes on the GPU{' in one piece' if count else ''} "
+                         f"are needed, not {tuple(p.shape)} of {p.dtype} on {p.device} with strides {p.stride()}")
+    return p.data_ptr()
+
+
+def _same_device(cache, p) -> None:
+    """The cache's tensors, p and the current device (on which the call launches) are one."""
+    if cache.device is not None and hasattr(p, "get_device"):
+        if not cache.device == p.get_device() == sys.modules["torch"].cuda.current_device():
+            raise ValueError(f"the cache is on cuda:{cache.device}, the call's tensors on {p.device}, the current device "
+                             f"is cuda:{sys.modules['torch'].cuda.current_device()}")
 
 
 def _stream(s) -> int:
@@ -283,10 +297,10 @@ def lwq_kv_append(cache: lwq_paged, rope, src: int, q, ldq: int, k, ldk: int, v,
                   cu_tokens=None, positions=None, stream=None) -> None:
     """Rotate q and k by position (rope None: not) and store k and v in the cache (see include/lwq.h)."""
     es = 4 if src == LWQ_ACT_F32 else 2
-    _check(_lib.lwq_kv_append(cache.at, None if rope is None else rope.at, src, _tensor(q, "q", es, 0, False), ldq,
-                              _tensor(k, "k", es, 0, False), ldk, _tensor(v, "v", es, 0, False), ldv,
-                              _tensor(q_out, "q_out", 2, T * H * cache.D),
-                              _tensor(cu_tokens, "cu_tokens", 4, cache.B + 1),
+    _same_device(cache, k)
+    _check(_lib.lwq_kv_append(cache.at, None if rope is None else rope.at, src, _tensor(q, "q", es), ldq,
+                              _tensor(k, "k", es), ldk, _tensor(v, "v", es), ldv,
+                              _tensor(q_out, "q_out", 2, T * H * cache.D), _tensor(cu_tokens, "cu_tokens", 4),
                               _tensor(positions, "positions", 4, T * (1 if rope is None else rope.axes)), T, H,
                               _stream(stream)), "lwq_kv_append")
 
@@ -298,6 +312,7 @@ def lwq_attention_paged_workspace_size(cache: lwq_paged, H: int) -> int:
 def lwq_attention_paged(cache: lwq_paged, q, out, H: int, scale: float, flags: int = 0, stream=None) -> None:
     """Decode attention, one query token per sequence, over the paged cache and its shared prefix."""
     n = cache.B * H * cache.D
+    _same_device(cache, q)
     _check(_lib.lwq_attention_paged(cache.at, flags, _tensor(q, "q", 2, n),
                                     _tensor(out, "out", 2 if flags & LWQ_FLAG_OUT16 else 4, n), H, float(scale),
                                     _stream(stream)), "lwq_attention_paged")
@@ -311,6 +326,7 @@ def lwq_attention_prefill(cache: lwq_paged, q, out, cu_tokens, T: int, H: int, s
                           stream=None) -> None:
     """Causal attention of the batch's new tokens over the cache that already holds them."""
     n = T * H * cache.D
+    _same_device(cache, q)
     _check(_lib.lwq_attention_prefill(cache.at, flags, _tensor(q, "q", 2, n),
                                       _tensor(out, "out", 2 if flags & LWQ_FLAG_OUT16 else 4, n),
                                       _tensor(cu_tokens, "cu_tokens", 4, cache.B + 1), T, H, float(scale),
