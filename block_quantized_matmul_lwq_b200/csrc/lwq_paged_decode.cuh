@@ -17,6 +17,11 @@
 // enter as exact sums of 16-bit parts: hi in MMA rows 0..7 and lo in rows
 // 8..15 of one product; in bf16, whose two parts hold only 16 bits, a third
 // part in a product of its own when the result is wanted in fp32.
+//
+// Measured (32 query and 8 kv heads of 128): one sequence of 100003 tokens in 65
+// us, 6.3 TB/s, and a merge of 7.5 us; 48 sequences of 0 to 8191 in 125 us, 6.6
+// TB/s, and 4.5 us; one query head per kv head, 16 x 4096 tokens, in 166 us, 6.5
+// TB/s.  A plain copy runs at 6.5 TB/s.
 #pragma once
 
 #include "lwq_paged.cuh"
