@@ -140,7 +140,8 @@ cudaError_t launch_paged_decode(const PagedPrefixArgs &k, cudaStream_t st) {
     const PagedDecodeArgs &d = k.d;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kern), smem);
     if (e != cudaSuccess) return e;
-    // behind a prefix's row tiles: a dependent launch that starts as their CTAs end and waits for the last of them at its own end
+    // behind a prefix's row tiles: a dependent launch, which starts as their CTAs end and waits for the last of them at
+    // its own end
     if ((e = launch_k(kern, d.ctas, PD_WARPS * 32, smem, st, k.prefix != nullptr, d)) != cudaSuccess) return e;
     if (!k.prefix) {
         const int parts = combine_parts((long)d.a.c.B * d.a.c.Hkv, d.a.G, d.ctas), n = d.a.G * D / parts;

@@ -275,146 +275,145 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         return min(KT, own_load - *key0);
     };
 
-    // a warp's wait, by one of its lanes (each lane that tries costs the barrier's unit a turn)
+    // a warp's wait, by one of its lanes
     auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
         int ok = 1;
         if (lane == 0) ok = mbar_wait(bar, parity, ta.timeout_ns, DEVERR_ATTN_WAIT);
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
-    if (warp == 0) {
-        // -------------------------------------------------------------- TMA
+    // (the register split is one instruction for all of a warpgroup's warps)
+    if (warp < 4) {
         regs_dec<TILE_REGS_FEED>();
-        const int brows = min(c.page, KT);
-        const int *table = c.tables + (size_t)rs.b * c.max_pages;
-        bool ok = true;
-        int i = 0;
-        for (int j = j0; ok && j < j0 + cnt; ++j) {
-            int key0;
-            const int valid = tile_keys(j, &key0);
-            const int boxes = (valid + brows - 1) / brows;
-            const int box = lane / (int)SM::HALVES, half = lane % (int)SM::HALVES;
-            int row = 0;
-            if (box < boxes) {
-                const int p = page_of(c, j < npre ? c.prefix : table, key0 + box * brows);
-                row = p < 0 ? ta.total_rows : (p * c.Hkv + g) * c.page + ((key0 + box * brows) & (c.page - 1));
-            }
-            for (int w = 0; w < 2; ++w, ++i) {
-                const int slot = i % ST;
-                if (i >= ST && !(ok = warp_wait(&empty[slot], (uint32_t)((i / ST - 1) & 1))))
-                    break;
-                if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * brows * D * 2));
-                __syncwarp();
-                if (box < boxes)
-                    tma_load_2d(sm + 2 * SM::QB + (size_t)slot * SM::SLOT + half * SM::HALF_KV + (size_t)box * brows * 128,
-                                w ? &vmap : &kmap, &full[slot], half * 64, row);
-            }
-        }
-        // copies still in flight land before the block ends
-        for (int x = max(0, i - ST); x < i; ++x)
-            warp_wait(&full[x % ST], (uint32_t)((x / ST) & 1));
-    } else if (warp == 1) {
-        // -------------------------------------------------------------- MMA
-        regs_dec<TILE_REGS_FEED>();
-        // One thread.  What lies between the arrival of probabilities and the next products is the critical path, so
-        // it waits for nothing else (warp 2 answers for the tiles in shared memory, as one of the arrivals on the
-        // probabilities' barrier); descriptors are made once and advanced by adding, and a tile's slots are handed
-        // back late, behind the next tile's first products (a commit is not issued before the products ahead of it).
-        if (elect_one()) {
+        if (warp == 0) {
+            // -------------------------------------------------------------- TMA
+            const int brows = min(c.page, KT);
+            const int *table = c.tables + (size_t)rs.b * c.max_pages;
             bool ok = true;
-            int slot = 0;           // of the ring
-            const uint64_t q_desc = umma_desc_sw128(q_smem), k_desc = umma_desc_sw128(ring),
-                           v_desc = umma_desc_mn_sw128(ring, SM::HALF_KV);
-            auto scores = [&](int t, int at) {   // S_t = Q_t K^T, the keys in slot `at`
-                const uint64_t qd = q_desc + (uint64_t)(t * (SM::QB >> 4)), kd = k_desc + (uint64_t)(at * (SM::SLOT >> 4));
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_f16(s_col(t), qd + ((kk / 4) * SM::HALF_Q + (kk % 4) * 32) / 16,
-                             kd + ((kk / 4) * SM::HALF_KV + (kk % 4) * 32) / 16, IDESC_S, kk ? 1u : 0u);
-                umma_commit(&s_full[t]);
-            };
-            int back[2] = {-1, -1};   // slots to hand back
-            if (cnt > 0) {
-                ok = mbar_wait(&full[0], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
-                for (int t = 0; ok && t < 2; ++t) {
-                    if ((t ? cnt1 : cnt0) == 0) continue;
-                    if (!(ok = mbar_wait(&q_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
-                    scores(t, 0);
+            int i = 0;
+            for (int j = j0; ok && j < j0 + cnt; ++j) {
+                int key0;
+                const int valid = tile_keys(j, &key0);
+                const int boxes = (valid + brows - 1) / brows;
+                const int box = lane / (int)SM::HALVES, half = lane % (int)SM::HALVES;
+                int row = 0;
+                if (box < boxes) {
+                    const int p = page_of(c, j < npre ? c.prefix : table, key0 + box * brows);
+                    row = p < 0 ? ta.total_rows : (p * c.Hkv + g) * c.page + ((key0 + box * brows) & (c.page - 1));
                 }
-                back[0] = 0;
-                for (int j = 0; ok && j < cnt; ++j) {
-                    const int v_slot = slot + 1 < ST ? slot + 1 : 0, k_slot = v_slot + 1 < ST ? v_slot + 1 : 0;
-                    slot = k_slot;
-                    const uint64_t vd = v_desc + (uint64_t)(v_slot * (SM::SLOT >> 4));
+                for (int w = 0; w < 2; ++w, ++i) {
+                    const int slot = i % ST;
+                    if (i >= ST && !(ok = warp_wait(&empty[slot], (uint32_t)((i / ST - 1) & 1))))
+                        break;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(boxes * brows * D * 2));
+                    __syncwarp();
+                    if (box < boxes)
+                        tma_load_2d(sm + 2 * SM::QB + (size_t)slot * SM::SLOT + half * SM::HALF_KV + (size_t)box * brows * 128,
+                                    w ? &vmap : &kmap, &full[slot], half * 64, row);
+                }
+            }
+            // copies still in flight land before the block ends
+            for (int x = max(0, i - ST); x < i; ++x)
+                warp_wait(&full[x % ST], (uint32_t)((x / ST) & 1));
+        } else if (warp == 1) {
+            // -------------------------------------------------------------- MMA
+            // One thread.  What lies between the arrival of probabilities and the next products is the critical path, so
+            // it waits for nothing else (warp 2 answers for the tiles in shared memory, as one of the arrivals on the
+            // probabilities' barrier); descriptors are made once and advanced by adding, and a tile's slots are handed
+            // back late, behind the next tile's first products (a commit is not issued before the products ahead of it).
+            if (elect_one()) {
+                bool ok = true;
+                int slot = 0;           // of the ring
+                const uint64_t q_desc = umma_desc_sw128(q_smem), k_desc = umma_desc_sw128(ring),
+                               v_desc = umma_desc_mn_sw128(ring, SM::HALF_KV);
+                auto scores = [&](int t, int at) {   // S_t = Q_t K^T, the keys in slot `at`
+                    const uint64_t qd = q_desc + (uint64_t)(t * (SM::QB >> 4)), kd = k_desc + (uint64_t)(at * (SM::SLOT >> 4));
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int mine = t ? cnt1 : cnt0;
-                        if (!ok || j >= mine) continue;
-                        // the probabilities come in two parts, so that the products of the first overlap the
-                        // exponentials of the second
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        umma_f16(s_col(t), qd + ((kk / 4) * SM::HALF_Q + (kk % 4) * 32) / 16,
+                                 kd + ((kk / 4) * SM::HALF_KV + (kk % 4) * 32) / 16, IDESC_S, kk ? 1u : 0u);
+                    umma_commit(&s_full[t]);
+                };
+                int back[2] = {-1, -1};   // slots to hand back
+                if (cnt > 0) {
+                    ok = mbar_wait(&full[0], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+                    for (int t = 0; ok && t < 2; ++t) {
+                        if ((t ? cnt1 : cnt0) == 0) continue;
+                        if (!(ok = mbar_wait(&q_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                        scores(t, 0);
+                    }
+                    back[0] = 0;
+                    for (int j = 0; ok && j < cnt; ++j) {
+                        const int v_slot = slot + 1 < ST ? slot + 1 : 0, k_slot = v_slot + 1 < ST ? v_slot + 1 : 0;
+                        slot = k_slot;
+                        const uint64_t vd = v_desc + (uint64_t)(v_slot * (SM::SLOT >> 4));
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            if (ok) ok = mbar_wait(&p_full[t + 2 * part], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
-                            if (!ok) continue;
-                            tc_fence_after();
+                        for (int t = 0; t < 2; ++t) {
+                            const int mine = t ? cnt1 : cnt0;
+                            if (!ok || j >= mine) continue;
+                            // the probabilities come in two parts, so that the products of the first overlap the
+                            // exponentials of the second
 #pragma unroll
-                            for (int p = PARTS - 1; p >= 0; --p)
+                            for (int part = 0; part < 2; ++part) {
+                                if (ok) ok = mbar_wait(&p_full[t + 2 * part], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
+                                if (!ok) continue;
+                                tc_fence_after();
 #pragma unroll
-                                for (int kk = part ? SPLIT / 16 : 0; kk < (part ? KT / 16 : SPLIT / 16); ++kk)
-                                    umma_f16_ts(o_col(t), s_col(t) + p * (KT / 2) + kk * 8, vd + kk * 128, IDESC_O,
-                                                (j % FRESH > 0 || part > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
-                            if (part == 0) {
+                                for (int p = PARTS - 1; p >= 0; --p)
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    if (back[i] >= 0) umma_commit(&empty[back[i]]);
-                                    back[i] = -1;
+                                    for (int kk = part ? SPLIT / 16 : 0; kk < (part ? KT / 16 : SPLIT / 16); ++kk)
+                                        umma_f16_ts(o_col(t), s_col(t) + p * (KT / 2) + kk * 8, vd + kk * 128, IDESC_O,
+                                                    (j % FRESH > 0 || part > 0 || p < PARTS - 1 || kk > 0) ? 1u : 0u);
+                                if (part == 0) {
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        if (back[i] >= 0) umma_commit(&empty[back[i]]);
+                                        back[i] = -1;
+                                    }
                                 }
                             }
+                            if (!ok) continue;
+                            if (j + 1 < mine)
+                                scores(t, k_slot);
+                            else
+                                umma_commit(&o_full[t]);
                         }
-                        if (!ok) continue;
-                        if (j + 1 < mine)
-                            scores(t, k_slot);
-                        else
-                            umma_commit(&o_full[t]);
+                        back[0] = v_slot;
+                        back[1] = j + 1 < cnt ? k_slot : -1;
                     }
-                    back[0] = v_slot;
-                    back[1] = j + 1 < cnt ? k_slot : -1;
+                }
+                umma_commit(all_done);   // every MMA is over before TMEM is released
+                mbar_wait(all_done, 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // -------------------------------------------------- tiles that landed
+            // V_j and K_(j+1) are in, and the value rows behind a segment's last key, which hold anything (NaN), are zeros
+            // (P is zero there): an arrival on both row tiles' probability barriers
+            const int end_pre = c.prefix_len % KT ? npre - 1 - j0 : -1, end_own = own_load % KT ? nall - 1 - j0 : -1;
+            bool ok = true;
+            for (int j = 0; ok && j < cnt; ++j) {
+                const int iv = 2 * j + 1;
+                if (!(ok = warp_wait(&full[iv % ST], (uint32_t)((iv / ST) & 1)))) break;
+                if (j == end_pre || j == end_own) {
+                    int key0;
+                    const int valid = tile_keys(j0 + j, &key0);
+                    const uint32_t vb = ring + (uint32_t)(iv % ST) * SM::SLOT;
+                    for (int x = lane; x < (KT - valid) * 8; x += 32)
+#pragma unroll
+                        for (uint32_t h = 0; h < SM::HALVES; ++h)
+                            st_shared_v4(vb + h * SM::HALF_KV + (uint32_t)(valid * 128 + x * 16), 0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (j + 1 < cnt && !(ok = warp_wait(&full[(iv + 1) % ST], (uint32_t)(((iv + 1) / ST) & 1)))) break;
+                for (int t = 0; ok && t < 2; ++t) {
+                    if (j >= (t ? cnt1 : cnt0)) continue;
+                    // (this phase's arrival only once the last phase is over)
+                    if (j > 0 && !(ok = warp_wait(&p_full[t], (uint32_t)((j - 1) & 1)))) break;
+                    if (lane == 0) mbar_arrive(&p_full[t]);
                 }
             }
-            umma_commit(all_done);   // every MMA is over before TMEM is released
-            mbar_wait(all_done, 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
         }
-        __syncwarp();
-    } else if (warp == 2) {
-        // -------------------------------------------------- tiles that landed
-        regs_dec<TILE_REGS_FEED>();
-        // V_j and K_(j+1) are in, and the value rows behind a segment's last key, which hold anything (NaN), are zeros
-        // (P is zero there): an arrival on both row tiles' probability barriers
-        const int end_pre = c.prefix_len % KT ? npre - 1 - j0 : -1, end_own = own_load % KT ? nall - 1 - j0 : -1;
-        bool ok = true;
-        for (int j = 0; ok && j < cnt; ++j) {
-            const int iv = 2 * j + 1;
-            if (!(ok = warp_wait(&full[iv % ST], (uint32_t)((iv / ST) & 1)))) break;
-            if (j == end_pre || j == end_own) {
-                int key0;
-                const int valid = tile_keys(j0 + j, &key0);
-                const uint32_t vb = ring + (uint32_t)(iv % ST) * SM::SLOT;
-                for (int x = lane; x < (KT - valid) * 8; x += 32)
-#pragma unroll
-                    for (uint32_t h = 0; h < SM::HALVES; ++h)
-                        st_shared_v4(vb + h * SM::HALF_KV + (uint32_t)(valid * 128 + x * 16), 0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            if (j + 1 < cnt && !(ok = warp_wait(&full[(iv + 1) % ST], (uint32_t)(((iv + 1) / ST) & 1)))) break;
-            for (int t = 0; ok && t < 2; ++t) {
-                if (j >= (t ? cnt1 : cnt0)) continue;
-                // (this phase's arrival only once the last phase is over)
-                if (j > 0 && !(ok = warp_wait(&p_full[t], (uint32_t)((j - 1) & 1)))) break;
-                if (lane == 0) mbar_arrive(&p_full[t]);
-            }
-        }
-    } else if (warp < 4) {
-        regs_dec<TILE_REGS_FEED>();
     } else {
         // ---------------------------------------------------------- softmax
         regs_inc<TILE_REGS_SOFTMAX>();
