@@ -218,7 +218,7 @@ struct PagedAttnArgs {
     const uint16_t *q;
     void *out;
     const int *cu;      // null: one query per sequence
-    int T, H, G, causal;
+    int T, H, G;
     int out16;
     float qscale;       // scale * log2(e)
 };

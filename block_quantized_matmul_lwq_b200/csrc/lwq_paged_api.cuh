@@ -97,7 +97,7 @@ cudaError_t launch_append_xt(int dtype, int D, const AppendArgs &a, const lwq_ro
 
 // The checks that both attention calls make, and the kernels' view of the arguments.
 int paged_attn_args(const lwq_paged *c, int flags, const void *q, void *out, const int32_t *cu, int T, int H,
-                    float scale, int causal, PagedAttnArgs *a) {
+                    float scale, PagedAttnArgs *a) {
     int rc = paged_sizes(c, H);
     if (rc) return rc;
     if (T <= 0 || !q || !out || (!cu && T != c->B) || !isfinite(scale)) return LWQ_ERR_INVALID_ARG;
@@ -112,7 +112,6 @@ int paged_attn_args(const lwq_paged *c, int flags, const void *q, void *out, con
     a->T = T;
     a->H = H;
     a->G = H / c->Hkv;
-    a->causal = causal;
     a->out16 = (flags & LWQ_FLAG_OUT16) ? 1 : 0;
     a->qscale = scale * 1.4426950408889634f;   // log2(e): the kernels take exponentials as exp2
     if (!isfinite(a->qscale)) return LWQ_ERR_INVALID_ARG;
@@ -370,7 +369,7 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
                         void *stream) {
     t_last_launches = 0;
     PagedAttnArgs a;
-    int rc = paged_attn_args(cache, flags, q, out, nullptr, cache ? cache->B : 0, H, scale, 0, &a);
+    int rc = paged_attn_args(cache, flags, q, out, nullptr, cache ? cache->B : 0, H, scale, &a);
     if (rc) return rc;
     int dev;
     if ((rc = current_device(&dev))) return rc;
@@ -422,7 +421,7 @@ int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void
                           int T, int H, float scale, void *stream) {
     t_last_launches = 0;
     PagedAttnArgs a;
-    int rc = paged_attn_args(cache, flags, q, out, cu_tokens, T, H, scale, 1, &a);
+    int rc = paged_attn_args(cache, flags, q, out, cu_tokens, T, H, scale, &a);
     if (rc) return rc;
     int dev;
     if ((rc = current_device(&dev))) return rc;

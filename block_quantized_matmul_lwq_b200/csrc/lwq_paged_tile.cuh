@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     // a warp's wait, by one of its lanes
     auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
         int ok = 1;
-        if (lane == 0) ok = mbar_wait(bar, parity, ta.timeout_ns, DEVERR_ATTN_WAIT);
+        if (lane == 0) ok = mbar_wait_near(bar, parity, ta.timeout_ns, DEVERR_ATTN_WAIT);
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
     // (the register split is one instruction for all of a warpgroup's warps)
@@ -335,10 +335,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 };
                 int back[2] = {-1, -1};   // slots to hand back
                 if (cnt > 0) {
-                    ok = mbar_wait(&full[0], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+                    ok = mbar_wait_near(&full[0], 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
                     for (int t = 0; ok && t < 2; ++t) {
                         if ((t ? cnt1 : cnt0) == 0) continue;
-                        if (!(ok = mbar_wait(&q_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                        if (!(ok = mbar_wait_near(&q_full[t], 0, ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
                         scores(t, 0);
                     }
                     back[0] = 0;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                             // exponentials of the second
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
-                                if (ok) ok = mbar_wait(&p_full[t + 2 * part], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
+                                if (ok) ok = mbar_wait_near(&p_full[t + 2 * part], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT);
                                 if (!ok) continue;
                                 tc_fence_after();
 #pragma unroll
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     }
                 }
                 umma_commit(all_done);   // every MMA is over before TMEM is released
-                mbar_wait(all_done, 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
+                mbar_wait_near(all_done, 0, ta.timeout_ns, DEVERR_ATTN_WAIT);
             }
             __syncwarp();
         } else if (warp == 2) {
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             row32 = static_cast<float *>(a.out) + at;
         bool ok = true;
         for (int j = 0; j < mine; ++j) {
-            if (!(ok = mbar_wait(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+            if (!(ok = mbar_wait_near(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
             tc_fence_after();
             const bool fresh = PARTS > 1 && j > 0 && j % FRESH == 0;
             if (fresh) {

@@ -89,7 +89,7 @@ constexpr uint32_t kWaitHintNs = 20000;
 // timeout_ns nanoseconds.  Returns false (after setting `errbit` in the device
 // error word) when the bound runs out; the caller then stops its loop.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64_t timeout_ns, unsigned errbit) {
-    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
         if (mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
@@ -98,6 +98,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
             return false;
         }
     }
+}
+
+// The same for waits that are mostly over when they begin, on a chain of short steps: the rest of it is laid out of the
+// way.
+__device__ __forceinline__ bool mbar_wait_near(uint64_t *bar, uint32_t parity, uint64_t timeout_ns, unsigned errbit) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    return mbar_wait(bar, parity, timeout_ns, errbit);
 }
 
 // One lane of a converged warp (always the same one): the compiler knows that a single thread runs what follows.
