@@ -14,9 +14,13 @@
 // pages are at least 16 tokens) through its own cp.async ring, which runs
 // ahead across units and pairs: the tensor cores form S = Q K^T and O += P V
 // with mma.sync (m16n8k16), rows being the query heads.  The probabilities
-// enter as exact sums of 16-bit parts: hi in MMA rows 0..7 and lo in rows
-// 8..15 of one product; in bf16, whose two parts hold only 16 bits, a third
-// part in a product of its own when the result is wanted in fp32.
+// enter as sums of 16-bit parts: hi in MMA rows 0..7 and lo in rows 8..15 of
+// one product; in bf16, whose two parts hold only 16 bits, a third part in a
+// product of its own when the result is wanted in fp32.  fp16's parts end at
+// 2^-24, whatever the probability, so they are taken of 2^15 p, the most that
+// fp16 holds for p <= 1: 22 bits of every p above 2^-17 of a warp's largest, an
+// error below 2^-40 of the largest for the others.  (Of p itself, the keys
+// behind one that is e^16 above them lost up to half their weight.)
 //
 // Measured (32 query and 8 kv heads of 128): one sequence of 100003 tokens in 65
 // us, 6.3 TB/s, and a merge of 7.5 us; 48 sequences of 0 to 8191 in 125 us, 6.6
@@ -101,6 +105,7 @@ template <int XT, int D, int NG, int PARTS>
 __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const PagedDecodeArgs d) {
     using SM = PagedDecodeSmem<D, NG>;
     constexpr int ST = SM::STAGES, NCH = D / 8;
+    constexpr float LIFT = XT == X_F16 ? 32768.f : 1.f;   // of the probabilities' parts, and so of o
     constexpr uint32_t ROWB = SM::ROWB, TILEB = SM::TILEB, STAGEB = SM::STAGEB;
     extern __shared__ __align__(128) uint8_t dsm[];
     // the scan's words, in the dynamic space (its limit is raised to all that a block may have)
@@ -265,6 +270,8 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
                 }
                 l[gg] = fmaf(l[gg], corr[gg], ps);
                 m[gg] = mn;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] *= LIFT;
                 const uint32_t h0 = pack16<XT>(p[0], p[1]), h1 = pack16<XT>(p[2], p[3]);
                 const float r0 = p[0] - lo16<XT>(h0), r1 = p[1] - hi16<XT>(h0);
                 const float r2 = p[2] - lo16<XT>(h1), r3 = p[3] - hi16<XT>(h1);
@@ -332,7 +339,8 @@ __global__ void __launch_bounds__(PD_WARPS * 32) paged_decode_kernel(const Paged
                 for (int n = 0; n < D / 8; ++n)   // hi rows + lo rows
                     if (h < G)
                         *reinterpret_cast<float2 *>(&sm_o[warp][h][8 * n + 2 * t]) =
-                            make_float2(o[gg][n][0] + o[gg][n][2], o[gg][n][1] + o[gg][n][3]);
+                            make_float2((o[gg][n][0] + o[gg][n][2]) * (1.f / LIFT),
+                                        (o[gg][n][1] + o[gg][n][3]) * (1.f / LIFT));
             }
             __syncthreads();
             // a pair that this run began and finished is complete; any other is a part of one
