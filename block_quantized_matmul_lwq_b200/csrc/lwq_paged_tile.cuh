@@ -20,13 +20,15 @@
 //
 // The two row tiles alternate: while one's scores are in the softmax warps the
 // tensor core works on the other.  A row's output is rescaled only when its
-// running maximum has grown by more than 8 (log2 domain) over the one in use:
-// until then its probabilities may exceed 1, up to 256, which changes nothing
-// but their scale, in numerator and denominator alike.
+// running maximum has outgrown the one that its probabilities are taken
+// against (see TileRange): until then they are larger by a factor, in numerator
+// and denominator alike.
 //
 // The probabilities are PARTS 16-bit numbers each.  A 16-bit result takes one
 // part (off by half a step of that type per key, like the result's own
-// rounding); an fp32 result takes two in fp16 (22 bits), three in bf16 (24).
+// rounding); an fp32 result takes two in fp16 (22 bits; fp16's parts end at
+// 2^-24, whatever the probability, so they are taken of 2^11 to 2^15 p), three
+// in bf16 (24).
 // The tensor cores truncate what they add to O, which pulls every sum towards
 // zero by about 2^-24 per product of 16 keys; for an fp32 result O therefore
 // starts anew every 1024 keys and the sums so far are kept, in rounded fp32,
@@ -51,7 +53,22 @@ constexpr int TILE_THREADS = 384;
 // registers per thread after the split: 128 x 56 + 256 x 224 = 64512, the 384 x 168 of the launch
 constexpr int TILE_REGS_FEED = 56, TILE_REGS_SOFTMAX = 224;
 constexpr uint32_t TILE_TMEM_COLS = 512;
-constexpr float TILE_SLACK = 8.f;      // growth of a row's maximum that needs no rescaling
+// What a row's probabilities are taken against (m, in the log2 domain, as all exponents here): when its maximum `top` is
+// taken anew they begin at 2^LIFT, and until one would pass 2^ROOM a larger score changes nothing.
+//   bf16   has fp32's range: 0 and 8.
+//   fp16   ends at 2^-24 below and at 65504 above: ROOM is 15, the half that stays free being for the rounding of
+//          exponents up to EXACT in size.  Begun at 2^11, a row's weights are off by less than 2^-36 of its largest.
+//          Begun at 2^13 they outgrow the room so often that a prompt of 8192 tokens takes 1105 us instead of 915 (fp32
+//          results; 16-bit: 515 and 480).  But a key that stands alone above the tile's others by more than ALONE (an
+//          attention sink: nothing follows that comes near it) begins at 2^15, and they are off by 2^-40 of it: there
+//          the others' weights may be all that the result is made of, while without such a key weights within 2^-8 of
+//          the largest outweigh what is lost.  Beyond EXACT, where 15 would be lost in the rounding of the maximum
+//          itself, 0 and 2: scores of up to 2^27, off by up to 8 from their maximum, stay in the type.
+template <int XT>
+struct TileRange {
+    static constexpr float LIFT = XT == X_F16 ? 11.f : 0.f, ROOM = XT == X_F16 ? 15.f : 8.f;
+    static constexpr float ALONE = 8.f, ALONE_LIFT = 15.f, EXACT = 4194304.f, FAR_ROOM = 2.f;
+};
 
 struct PagedTileArgs {
     PagedAttnArgs a;
@@ -466,8 +483,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
         const uint32_t lane_off = (uint32_t)(32 * quarter) << 16;
         const uint32_t sc = s_col(t) + lane_off, oc = o_col(t) + lane_off;
-        float m = -INFINITY, l = 0.f;
-        // the row's place in fp32: a partial result's values, or the output's (kept is the maximum its sums refer to)
+        float m = -INFINITY, l = 0.f;   // m: what the exponents are taken against (see TileRange)
+        // the row's place in fp32: a partial result's values, or the output's (kept is the m its sums refer to)
         float *row32 = nullptr, kept = -INFINITY;
         const int ri = rs.row0 + r;
         const size_t at = live ? ((size_t)(rs.tok0 + ri / a.G) * a.H + (size_t)g * a.G + ri % a.G) * D : 0;
@@ -540,9 +557,17 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             }
             const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.qscale;
             // (the first tile with a live key sets m; O is overwritten by the first product)
-            const bool grown = top > m + TILE_SLACK || (m == -INFINITY && top > m);
+            using R = TileRange<XT>;
+            const float room = XT == X_F16 && fabsf(m) >= R::EXACT ? R::FAR_ROOM : R::ROOM;
+            const bool grown = top > m + room || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grown)) {
-                const float mn = grown ? top : m;
+                float lift = R::LIFT;
+                if constexpr (XT == X_F16) {
+                    // (mx: the maxima of four interleaved quarters of the tile's keys)
+                    if (top - fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * a.qscale > R::ALONE) lift = R::ALONE_LIFT;
+                    if (fabsf(top) >= R::EXACT) lift = 0.f;
+                }
+                const float mn = grown ? top - lift : m;
                 const float f = grown ? ex2(m - mn) : 1.f;          // 0 while m = -inf
                 m = mn;
                 l *= f;

@@ -67,7 +67,9 @@ def check(p, gap, causal, out16, lift):
     ref = expected(p, gap, causal)
     # 16-bit results below their type's normal range are multiples of its smallest step
     step = torch.finfo(out.dtype).smallest_normal * torch.finfo(out.dtype).eps if out16 else 0.0
-    err = float((((out.double() - ref).abs() - step) / ref).max())
+    alone = (ref == 0).expand(out.shape)                           # rows that see the sink only
+    assert (out[alone] == 0).all()
+    err = float((((out.double() - ref).abs() - step) / ref)[~alone].max())
     n = p.prefix + max(p.lens)
     assert err <= bound(p.dtype, gap, n, out16, lift), f"relative error {err:.3e}"
 
@@ -78,3 +80,59 @@ def check(p, gap, causal, out16, lift):
 def test_decode(dev, gap, dtype, out16):                           # noqa: F811
     check(sink_problem(dev, dtype, gap, [300, 4097, 65], 8, 2, 64, 16, seed=1), gap, False, out16, 15)
     check(sink_problem(dev, dtype, gap, [20000], 16, 1, 128, 64, seed=2), gap, False, out16, 15)
+
+
+@pytest.mark.parametrize("out16", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("gap", GAPS)
+def test_prefill(dev, gap, dtype, out16):                          # noqa: F811
+    """Whole and with the keys split."""
+    check(sink_problem(dev, dtype, gap, [300, 700, 65], 8, 2, 64, 16, new=[300, 130, 3], seed=3), gap, True, out16, 13)
+    check(sink_problem(dev, dtype, gap, [9000], 16, 1, 128, 64, new=[7], seed=4), gap, True, out16, 13)
+    check(sink_problem(dev, dtype, gap, [2500], 40, 40, 64, 64, new=[600], seed=5), gap, True, out16, 13)
+
+
+@pytest.mark.parametrize("out16", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("gap", GAPS)
+def test_prefix(dev, gap, dtype, out16):                           # noqa: F811
+    """The sink and most keys in the prefix, some of the sequences' own, some with none."""
+    check(sink_problem(dev, dtype, gap, [0, 300, 65], 8, 2, 64, 16, prefix=701, seed=6), gap, False, out16, 13)
+    check(sink_problem(dev, dtype, gap, [5] * 90, 8, 8, 128, 64, prefix=3001, seed=7), gap, False, out16, 13)
+
+
+@pytest.mark.parametrize("gap", [10.0, 14.0, 17.0])
+@pytest.mark.parametrize("count", [3, 9])
+def test_several_sinks(dev, gap, count):                           # noqa: F811
+    """The first keys alike: few leave some of the tile's quarters without one, nine do not (and begin at 2^11)."""
+    p = sink_problem(dev, "f16", gap, [3000], 8, 8, 128, 16, new=[40], seed=9)
+    p.kc[int(p.tables_h[0, 0]), :, :count, 0] = gap
+    p.vc[int(p.tables_h[0, 0]), :, :count] = 0.0
+    out = torch.full((p.T, p.H, p.D), float("nan"), device=dev)
+    lwq.lwq_attention_prefill(p.cache(), p.q, out, p.cu_d, p.T, p.H, p.scale)
+    torch.cuda.synchronize(dev)
+    n = torch.arange(2960, 3000, dtype=torch.float64, device=dev)[:, None, None] + 1 - count
+    ref = n / (n + count * math.exp(gap))
+    err = float(((out.double() - ref).abs() / ref).max())
+    assert err <= bound("f16", gap, 3000, False, 15 if count == 3 else 11), f"relative error {err:.3e}"
+
+
+def test_scores_far_beyond_the_lift(dev):                          # noqa: F811
+    """Scores of 2^24 and more, which leave no room for a shift of 15: the largest key alone counts (the next lies 2^15
+    or more behind it), whichever comes first, and nothing overflows."""
+    for size in (3.0e3, 1.2e4):
+        p = Problem(dev, "f16", [400], 4, 2, 64, 16, new=[40], seed=8, poison=False)
+        p.kc.zero_()
+        p.q.zero_()
+        p.q[..., 0] = size
+        p.scale = 8192.0
+        for j in range(400):
+            p.kc[p.tables_h[0, j // 16], :, j % 16, 0] = float(j % 7) * 0.125 + 0.5
+        out = torch.full((40, 4, 64), float("nan"), device=dev)
+        lwq.lwq_attention_prefill(p.cache(), p.q, out, p.cu_d, 40, 4, p.scale)
+        torch.cuda.synchronize(dev)
+        _, v = p.rows(0, 400)
+        for i in (0, 17, 39):
+            best = [j for j in range(361 + i) if j % 7 == 6]
+            want = v[:, best].mean(1).repeat_interleave(2, 0)
+            assert float((out[i].double() - want).abs().max()) < 1e-5
