@@ -30,10 +30,17 @@
 // 2^-24, whatever the probability, so they are taken of 2^11 to 2^15 p), three
 // in bf16 (24).
 // The tensor cores truncate what they add to O, which pulls every sum towards
-// zero by about 2^-24 per product of 16 keys; for an fp32 result O therefore
+// zero by about 2^-23 per product of 16 keys; for an fp32 result O therefore
 // starts anew every 1024 keys and the sums so far are kept, in rounded fp32,
 // in the row's place in the output (or among the partial results): 1 to 3e-6 of
-// the result at any length.
+// the result at any length.  For a 16-bit result it is relieved every 16384 keys
+// in fp16, every 32768 in bf16 (1e-4 and 2e-4 of the result, a fifth and a
+// twentieth of a half step; 131072 keys left to one accumulator took 8e-4, nearly
+// two half steps of fp16): the row's place in the output takes the sums so far
+// rounded to 16 bits, in units of a power of two that holds them, and O goes on
+// from the remainder, so that nothing is lost and no fp32 space is needed.  Each
+// time costs a CTA about 10 us (16384 tokens relieved every 8192 keys took 2.10
+// ms, never 2.01), so it is not done more often.
 //
 // Measured (32 query and 8 kv heads of 128, bf16): a prompt of 8192 tokens in
 // 455 us, 1.21 PFLOP/s, 0.72 of what a large matrix product reaches in a burst;
@@ -194,6 +201,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     static_assert(SM::STAGES >= 3, "K and V of a tile and the next K");
     constexpr int ST = SM::STAGES;
     constexpr int FRESH = PARTS > 1 ? 1024 / KT : 1 << 30;   // key tiles after which O starts anew
+    constexpr int RELIEF = (XT == X_F16 ? 16384 : 32768) / KT;   // with one part: after which it goes on from a remainder
     constexpr int SPLIT = KT == 128 ? 96 : 32;   // keys of the first part of the probabilities
     constexpr uint32_t IDESC_S = umma_idesc_f16(XT == X_F16 ? 0 : 1, TILE_ROWS, KT);
     constexpr uint32_t IDESC_O = umma_idesc_f16(XT == X_F16 ? 0 : 1, TILE_ROWS, D) | (1u << 16);   // B along N
@@ -492,147 +500,210 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             row32 = ta.part + (((size_t)(pair * c.Hkv + g) * ta.splits + split) * PAIR_ROWS + r) * part_stride(D) + 4;
         else if (!a.out16)
             row32 = static_cast<float *>(a.out) + at;
+        // with one part: what the row's place holds is in units of this
+        float unit = 1.f;
+        auto load_kept = [&](int x, float(&k)[8]) {
+            if (ta.part || PARTS > 1) {
+                const float4 u = __ldcg(reinterpret_cast<const float4 *>(row32 + x)),
+                             v = __ldcg(reinterpret_cast<const float4 *>(row32 + x + 4));
+                k[0] = u.x, k[1] = u.y, k[2] = u.z, k[3] = u.w;
+                k[4] = v.x, k[5] = v.y, k[6] = v.z, k[7] = v.w;
+            } else {
+                const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.out) + at + x));
+                k[0] = lo16<XT>(u.x), k[1] = hi16<XT>(u.x), k[2] = lo16<XT>(u.y), k[3] = hi16<XT>(u.y);
+                k[4] = lo16<XT>(u.z), k[5] = hi16<XT>(u.z), k[6] = lo16<XT>(u.w), k[7] = hi16<XT>(u.w);
+            }
+        };
         bool ok = true;
-        for (int j = 0; j < mine; ++j) {
-            if (!(ok = mbar_wait_near(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
-            tc_fence_after();
-            const bool fresh = PARTS > 1 && j > 0 && j % FRESH == 0;
-            if (fresh) {
-                // O's sums of the last tiles join those kept (the tensor core is done with O: it has formed S since).
-                // With the maximum unchanged since, as it mostly is, that is an addition in memory, which is not
-                // waited for; the row is this thread's alone, so the order of additions is fixed.
-                const float f = kept == -INFINITY ? 0.f : ex2(kept - m);
-                const int how = j == FRESH ? 0 : __all_sync(0xffffffffu, f == 1.f || !live) ? 1 : 2;
+        int j = 0;
+        while (j < mine) {
+            if (PARTS == 1 && j > 0) {
+                if (!(ok = mbar_wait_near(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                tc_fence_after();
+                // (the tensor core is done with O, as it has formed S since.)  |O| and what is kept stay below l times
+                // 65504, the largest value, so 16 bits hold their sum in units of 2 l or more; the remainder is exact
+                const float f = kept == -INFINITY ? 0.f : ex2(kept - m) * unit;
+                if (!ta.part) unit = __uint_as_float((__float_as_uint(l) & 0x7f800000u) + 0x01000000u);
+                const float per_unit = __uint_as_float(0x7f000000u - __float_as_uint(unit));
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
                     uint32_t o[32];
                     __syncwarp();
                     tmem_ld_32x32b_x32(oc + x, o);
                     tmem_wait_ld();
-                    if (!live) continue;
-                    float *p = row32 + x;
+                    if (live) {
 #pragma unroll
-                    for (int y = 0; y < 32; y += 4) {
-                        float4 v = make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]), __uint_as_float(o[y + 2]),
-                                               __uint_as_float(o[y + 3]));
-                        if (how == 1) {
-                            asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + y), "f"(v.x),
-                                         "f"(v.y), "f"(v.z), "f"(v.w)
-                                         : "memory");
-                            continue;
+                        for (int y = 0; y < 32; y += 8) {
+                            float k[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                            if (j > RELIEF) load_kept(x + y, k);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) k[e] = fmaf(k[e], f, __uint_as_float(o[y + e]));
+                            if (ta.part) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) o[y + e] = 0u;
+                                __stcg(reinterpret_cast<float4 *>(row32 + x + y), make_float4(k[0], k[1], k[2], k[3]));
+                                __stcg(reinterpret_cast<float4 *>(row32 + x + y + 4), make_float4(k[4], k[5], k[6], k[7]));
+                            } else {
+                                uint32_t h[4];
+#pragma unroll
+                                for (int e = 0; e < 8; e += 2) {
+                                    h[e / 2] = pack16<XT>(k[e] * per_unit, k[e + 1] * per_unit);
+                                    o[y + e] = __float_as_uint(fmaf(lo16<XT>(h[e / 2]), -unit, k[e]));
+                                    o[y + e + 1] = __float_as_uint(fmaf(hi16<XT>(h[e / 2]), -unit, k[e + 1]));
+                                }
+                                __stcg(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + x + y),
+                                       make_uint4(h[0], h[1], h[2], h[3]));
+                            }
                         }
-                        if (how == 2) {
-                            const float4 k = __ldcg(reinterpret_cast<const float4 *>(p + y));
-                            v = make_float4(fmaf(k.x, f, v.x), fmaf(k.y, f, v.y), fmaf(k.z, f, v.z), fmaf(k.w, f, v.w));
-                        }
-                        __stcg(reinterpret_cast<float4 *>(p + y), v);
                     }
+                    __syncwarp();
+                    tmem_st_32x32b_x32(oc + x, o);
                 }
-                __syncwarp();
+                tmem_wait_st();
                 kept = m;
             }
-            uint32_t s[KT];
-            int key0;
-            tile_keys(j0 + j, &key0);
-            const int limit = (j0 + j < npre ? pre : own) - key0;   // keys of the tile that the row sees
-            const bool cut = __any_sync(0xffffffffu, limit < KT);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int x = 0; x < 64; x += 32) tmem_ld_32x32b_x32(sc + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
-            tmem_wait_ld();
-            // the second half's scores arrive under the first's maximum
-#pragma unroll
-            for (int x = 64; x < KT; x += 32) tmem_ld_32x32b_x32(sc + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
-#pragma unroll
-            for (int x0 = 0; x0 < KT; x0 += 64) {
-                if (x0 > 0) tmem_wait_ld();
-                if (cut) {
-#pragma unroll
-                    for (int x = x0; x < x0 + 64; ++x)
-                        if (x >= limit) s[x] = 0xff800000u;         // -inf
-                }
-#pragma unroll
-                for (int x = x0; x < x0 + 64; x += 2)
-                    mx[(x / 2) & 3] = max3(mx[(x / 2) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
-            }
-            const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.qscale;
-            // (the first tile with a live key sets m; O is overwritten by the first product)
-            using R = TileRange<XT>;
-            const float room = XT == X_F16 && fabsf(m) >= R::EXACT ? R::FAR_ROOM : R::ROOM;
-            const bool grown = top > m + room || (m == -INFINITY && top > m);
-            if (__any_sync(0xffffffffu, grown)) {
-                float lift = R::LIFT;
-                if constexpr (XT == X_F16) {
-                    // (mx: the maxima of four interleaved quarters of the tile's keys)
-                    if (top - fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * a.qscale > R::ALONE) lift = R::ALONE_LIFT;
-                    if (fabsf(top) >= R::EXACT) lift = 0.f;
-                }
-                const float mn = grown ? top - lift : m;
-                const float f = grown ? ex2(m - mn) : 1.f;          // 0 while m = -inf
-                m = mn;
-                l *= f;
-                if (j > 0 && !fresh) {
-#pragma unroll
+            for (const int end = PARTS == 1 ? min(mine, j + RELIEF) : mine; j < end; ++j) {
+                if (!(ok = mbar_wait_near(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                tc_fence_after();
+                const bool fresh = PARTS > 1 && j > 0 && j % FRESH == 0;
+                if (fresh) {
+                    // O's sums of the last tiles join those kept (the tensor core is done with O: it has formed S since).
+                    // With the maximum unchanged since, as it mostly is, that is an addition in memory, which is not
+                    // waited for; the row is this thread's alone, so the order of additions is fixed.
+                    const float f = kept == -INFINITY ? 0.f : ex2(kept - m);
+                    const int how = j == FRESH ? 0 : __all_sync(0xffffffffu, f == 1.f || !live) ? 1 : 2;
+#pragma unroll 1
                     for (int x = 0; x < D; x += 32) {
                         uint32_t o[32];
+                        __syncwarp();
                         tmem_ld_32x32b_x32(oc + x, o);
                         tmem_wait_ld();
+                        if (!live) continue;
+                        float *p = row32 + x;
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                        tmem_st_32x32b_x32(oc + x, o);
+                        for (int y = 0; y < 32; y += 4) {
+                            float4 v = make_float4(__uint_as_float(o[y]), __uint_as_float(o[y + 1]), __uint_as_float(o[y + 2]),
+                                                   __uint_as_float(o[y + 3]));
+                            if (how == 1) {
+                                asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + y), "f"(v.x),
+                                             "f"(v.y), "f"(v.z), "f"(v.w)
+                                             : "memory");
+                                continue;
+                            }
+                            if (how == 2) {
+                                const float4 k = __ldcg(reinterpret_cast<const float4 *>(p + y));
+                                v = make_float4(fmaf(k.x, f, v.x), fmaf(k.y, f, v.y), fmaf(k.z, f, v.z), fmaf(k.w, f, v.w));
+                            }
+                            __stcg(reinterpret_cast<float4 *>(p + y), v);
+                        }
+                    }
+                    __syncwarp();
+                    kept = m;
+                }
+                uint32_t s[KT];
+                int key0;
+                tile_keys(j0 + j, &key0);
+                const int limit = (j0 + j < npre ? pre : own) - key0;   // keys of the tile that the row sees
+                const bool cut = __any_sync(0xffffffffu, limit < KT);
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int x = 0; x < 64; x += 32) tmem_ld_32x32b_x32(sc + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
+                tmem_wait_ld();
+                // the second half's scores arrive under the first's maximum
+#pragma unroll
+                for (int x = 64; x < KT; x += 32) tmem_ld_32x32b_x32(sc + x, *reinterpret_cast<uint32_t(*)[32]>(s + x));
+#pragma unroll
+                for (int x0 = 0; x0 < KT; x0 += 64) {
+                    if (x0 > 0) tmem_wait_ld();
+                    if (cut) {
+#pragma unroll
+                        for (int x = x0; x < x0 + 64; ++x)
+                            if (x >= limit) s[x] = 0xff800000u;         // -inf
+                    }
+#pragma unroll
+                    for (int x = x0; x < x0 + 64; x += 2)
+                        mx[(x / 2) & 3] = max3(mx[(x / 2) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                }
+                const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.qscale;
+                // (the first tile with a live key sets m; O is overwritten by the first product)
+                using R = TileRange<XT>;
+                const float room = XT == X_F16 && fabsf(m) >= R::EXACT ? R::FAR_ROOM : R::ROOM;
+                const bool grown = top > m + room || (m == -INFINITY && top > m);
+                if (__any_sync(0xffffffffu, grown)) {
+                    float lift = R::LIFT;
+                    if constexpr (XT == X_F16) {
+                        // (mx: the maxima of four interleaved quarters of the tile's keys)
+                        if (top - fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3])) * a.qscale > R::ALONE) lift = R::ALONE_LIFT;
+                        if (fabsf(top) >= R::EXACT) lift = 0.f;
+                    }
+                    const float mn = grown ? top - lift : m;
+                    const float f = grown ? ex2(m - mn) : 1.f;          // 0 while m = -inf
+                    m = mn;
+                    l *= f;
+                    if (j > 0 && !fresh) {
+#pragma unroll
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(oc + x, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                            tmem_st_32x32b_x32(oc + x, o);
+                        }
                     }
                 }
-            }
-            const float base = m == -INFINITY ? 0.f : m;            // a row that has seen nothing: all zeros
-            const uint64_t scale2 = pack2(a.qscale, a.qscale), base2 = pack2(-base, -base);
-            uint64_t sum2[2] = {0, 0};
+                const float base = m == -INFINITY ? 0.f : m;            // a row that has seen nothing: all zeros
+                const uint64_t scale2 = pack2(a.qscale, a.qscale), base2 = pack2(-base, -base);
+                uint64_t sum2[2] = {0, 0};
 #pragma unroll
-            for (int x0 = 0; x0 < KT; x0 += 32) {
-                uint32_t h[16];
-#pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                    const uint64_t y = fma2(pack2(__uint_as_float(s[x0 + x]), __uint_as_float(s[x0 + x + 1])), scale2, base2);
-                    float p0, p1;
-                    unpack2(y, p0, p1);
-                    p0 = ex2(p0);
-                    p1 = ex2(p1);
-                    sum2[(x / 2) & 1] = add2(sum2[(x / 2) & 1], pack2(p0, p1));
-                    h[x / 2] = pack16<XT>(p0, p1);
-                    if constexpr (PARTS > 1) {
-                        s[x0 + x] = __float_as_uint(p0 - lo16<XT>(h[x / 2]));
-                        s[x0 + x + 1] = __float_as_uint(p1 - hi16<XT>(h[x / 2]));
-                    }
-                }
-                tmem_st_32x32b_x16(sc + x0 / 2, h);
-#pragma unroll
-                for (int p = 1; p < PARTS; ++p) {
+                for (int x0 = 0; x0 < KT; x0 += 32) {
+                    uint32_t h[16];
 #pragma unroll
                     for (int x = 0; x < 32; x += 2) {
-                        const float r0 = __uint_as_float(s[x0 + x]), r1 = __uint_as_float(s[x0 + x + 1]);
-                        h[x / 2] = pack16<XT>(r0, r1);
-                        s[x0 + x] = __float_as_uint(r0 - lo16<XT>(h[x / 2]));
-                        s[x0 + x + 1] = __float_as_uint(r1 - hi16<XT>(h[x / 2]));
+                        const uint64_t y = fma2(pack2(__uint_as_float(s[x0 + x]), __uint_as_float(s[x0 + x + 1])), scale2, base2);
+                        float p0, p1;
+                        unpack2(y, p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum2[(x / 2) & 1] = add2(sum2[(x / 2) & 1], pack2(p0, p1));
+                        h[x / 2] = pack16<XT>(p0, p1);
+                        if constexpr (PARTS > 1) {
+                            s[x0 + x] = __float_as_uint(p0 - lo16<XT>(h[x / 2]));
+                            s[x0 + x + 1] = __float_as_uint(p1 - hi16<XT>(h[x / 2]));
+                        }
                     }
-                    tmem_st_32x32b_x16(sc + p * (KT / 2) + x0 / 2, h);
+                    tmem_st_32x32b_x16(sc + x0 / 2, h);
+#pragma unroll
+                    for (int p = 1; p < PARTS; ++p) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            const float r0 = __uint_as_float(s[x0 + x]), r1 = __uint_as_float(s[x0 + x + 1]);
+                            h[x / 2] = pack16<XT>(r0, r1);
+                            s[x0 + x] = __float_as_uint(r0 - lo16<XT>(h[x / 2]));
+                            s[x0 + x + 1] = __float_as_uint(r1 - hi16<XT>(h[x / 2]));
+                        }
+                        tmem_st_32x32b_x16(sc + p * (KT / 2) + x0 / 2, h);
+                    }
+                    if (x0 + 32 == SPLIT || x0 + 32 == KT) {   // a part is ready
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[t + (x0 + 32 == KT ? 2 : 0)]);
+                    }
                 }
-                if (x0 + 32 == SPLIT || x0 + 32 == KT) {   // a part is ready
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[t + (x0 + 32 == KT ? 2 : 0)]);
-                }
+                float l0, l1;
+                unpack2(add2(sum2[0], sum2[1]), l0, l1);
+    l += l0 + l1;
             }
-            float l0, l1;
-            unpack2(add2(sum2[0], sum2[1]), l0, l1);
-            l += l0 + l1;
+            if (!ok) break;
         }
         // ---------------------------------------------------------- results
         if (mine > 0 && ok) ok = warp_wait(&o_full[t], 0);
         tc_fence_after();
         if (ok) {
             if (ta.part && live) *reinterpret_cast<float2 *>(row32 - 4) = make_float2(m, l);
-            const bool more = PARTS > 1 && mine > FRESH;        // sums were kept
-            const float fk = more && kept != -INFINITY ? ex2(kept - m) : 0.f;
+            const bool more = mine > (PARTS > 1 ? FRESH : RELIEF);   // sums were kept
+            const float fk = more && kept != -INFINITY ? ex2(kept - m) * unit : 0.f;
             const float inv = ta.part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
 #pragma unroll
             for (int x0 = 0; x0 < D; x0 += 32) {
@@ -651,12 +722,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(o[x]);
                 if (more) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4) {
-                        const float4 k = __ldcg(reinterpret_cast<const float4 *>(row32 + x0 + x));
-                        f[x] = fmaf(k.x, fk, f[x]);
-                        f[x + 1] = fmaf(k.y, fk, f[x + 1]);
-                        f[x + 2] = fmaf(k.z, fk, f[x + 2]);
-                        f[x + 3] = fmaf(k.w, fk, f[x + 3]);
+                    for (int x = 0; x < 32; x += 8) {
+                        float k[8];
+                        load_kept(x0 + x, k);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[x + e] = fmaf(k[e], fk, f[x + e]);
                     }
                 }
 #pragma unroll
