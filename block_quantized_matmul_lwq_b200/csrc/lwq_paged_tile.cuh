@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                       const PagedTileArgs ta) {
     using SM = TileSmem<D, KT>;
     static_assert(PARTS * KT / 2 <= 128 && KT <= 128 && KT % 64 == 0, "a tile's scores and probabilities share 128 columns");
-    static_assert(SM::STAGES >= 3, "K and V of a tile and the next K");
+    static_assert(SM::STAGES >= 4, "V and the next K land before a tile's products, which hand back the V before them");
     constexpr int ST = SM::STAGES;
     constexpr int FRESH = PARTS > 1 ? 1024 / KT : 1 << 30;   // key tiles after which O starts anew
     constexpr int RELIEF = (XT == X_F16 ? 16384 : 32768) / KT;   // with one part: after which it goes on from a remainder
