@@ -306,6 +306,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (lane == 0) ok = mbar_wait_near(bar, parity, ta.timeout_ns, DEVERR_ATTN_WAIT);
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     };
+    // one by all of its lanes, each on its own, as a chain of short steps wants it; they agree on how it ended, since what
+    // follows takes the whole warp (near the limit some could give up and others not)
+    auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_near(bar, parity, ta.timeout_ns, DEVERR_ATTN_WAIT)) != 0;
+    };
     // (the register split is one instruction for all of a warpgroup's warps)
     if (warp < 4) {
         regs_dec<TILE_REGS_FEED>();
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         int j = 0;
         while (j < mine) {
             if (PARTS == 1 && j > 0) {
-                if (!(ok = mbar_wait_near(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                if (!(ok = all_wait(&s_full[t], (uint32_t)(j & 1)))) break;
                 tc_fence_after();
                 // (the tensor core is done with O, as it has formed S since.)  |O| and what is kept stay below l times
                 // 65504, the largest value, so 16 bits hold their sum in units of 2 l or more; the remainder is exact
@@ -563,7 +568,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 kept = m;
             }
             for (const int end = PARTS == 1 ? min(mine, j + RELIEF) : mine; j < end; ++j) {
-                if (!(ok = mbar_wait_near(&s_full[t], (uint32_t)(j & 1), ta.timeout_ns, DEVERR_ATTN_WAIT))) break;
+                if (!(ok = all_wait(&s_full[t], (uint32_t)(j & 1)))) break;
                 tc_fence_after();
                 const bool fresh = PARTS > 1 && j > 0 && j % FRESH == 0;
                 if (fresh) {

@@ -1,5 +1,6 @@
 """The row-tile kernel's waits, on the CPU: a model of its warps (tile copies, products, the warp that answers for landed
-tiles, softmax) with the ring's slots and the barriers between them, run until nobody can go on."""
+tiles, softmax) with the ring's slots and the barriers between them, run until nobody can go on; and the rule that a
+warp's lanes act on one outcome of a wait."""
 
 import os
 import re
@@ -96,3 +97,18 @@ def test_four_slots_and_more_end(stages):
 def test_the_least_number_of_slots_that_is_compiled_ends():
     least = int(re.search(r"static_assert\(SM::STAGES >= (\d+)", source()).group(1))
     assert all(pipeline_ends(least, c) for c in COUNTS)
+
+
+def test_a_softmax_warp_acts_on_one_outcome_of_a_wait():
+    """A wait that runs out ends with a result, in each lane its own: between the softmax warps' start and end only the
+    two waits whose outcome the warp shares are made, or lanes that gave up would leave the others in instructions of
+    the whole warp."""
+    text = source()
+    softmax = text[text.index("regs_inc<TILE_REGS_SOFTMAX>();"):]
+    softmax = softmax[:softmax.index("    __syncthreads();\n    if (warp == 1) {")]
+    waits = re.findall(r"\b(\w*_wait(?:_near)?)\(", softmax)
+    assert waits and set(waits) == {"all_wait", "warp_wait"}
+    body = text[text.index("auto all_wait ="):]
+    assert "return __all_sync(0xffffffffu, mbar_wait_near(" in body[:body.index("};")]
+    body = text[text.index("auto warp_wait ="):]
+    assert "if (lane == 0) ok =" in body[:body.index("};")] and "return __shfl_sync(" in body[:body.index("};")]
