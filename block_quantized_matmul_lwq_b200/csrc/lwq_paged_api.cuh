@@ -77,6 +77,29 @@ int rope_check(const lwq_rope *r, int D) {
     return LWQ_OK;
 }
 
+// f / (2 pi) modulo 1 in units of 2^-64, rounded to nearest, |f| below 2^63: all 64 bits of f's significand times 192
+// bits of 1 / (2 pi) in integers (a quotient in floating point would lose below what the whole turns leave).
+uint64_t turn_of(long double f) {
+    constexpr uint64_t inv[3] = {0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};   // lowest first
+    int e;
+    const uint64_t m = (uint64_t)ldexpl(frexpl(fabsl(f), &e), 64);   // |f| = m 2^(e - 64)
+    uint64_t p[5] = {};                                              // m / (2 pi) in units of 2^-192
+    unsigned __int128 carry = 0;
+    for (int i = 0; i < 3; ++i) {
+        carry += (unsigned __int128)m * inv[i];
+        p[i] = (uint64_t)carry;
+        carry >>= 64;
+    }
+    p[3] = (uint64_t)carry;
+    const int at = 192 - e;          // the bit of p that weighs 2^-64 turns
+    auto bits = [&](int k) {         // 64 bits of p from bit k on
+        const int w = k / 64, b = k % 64;
+        return w > 3 ? 0 : b ? p[w] >> b | p[w + 1] << (64 - b) : p[w];
+    };
+    const uint64_t u = bits(at) + (bits(at - 1) & 1);
+    return f < 0 ? 0 - u : u;
+}
+
 template <int ST, int XT>
 cudaError_t launch_append(int D, const AppendArgs &a, const lwq_rope &rope, cudaStream_t st) {
     // a block per token (several where its rows need more than 8 warps): never less than the 64 threads of its pairs,
@@ -281,14 +304,10 @@ int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const do
         for (int i = 0; i < n; ++i) r.axis[at++] = (uint8_t)a;
     }
     if (at != half) return LWQ_ERR_INVALID_ARG;
-    const long double two_pi = 6.283185307179586476925286766559006L;
     for (int i = 0; i < half; ++i) {
         const long double f = inv_freq ? (long double)inv_freq[i] : powl((long double)base, -2.0L * i / rot_dim);
-        if (!isfinite(f) || fabsl(f) > 1048576.0L) return LWQ_ERR_INVALID_ARG;
-        long double t = f / two_pi;
-        t -= floorl(t);
-        const long double u = ldexpl(t, 64);   // in [0, 2^64]: a fraction that rounded up to 1 is 0 turns
-        r.turn[i] = u >= 18446744073709551615.0L ? 0 : (uint64_t)u;
+        if (!isfinite(f) || fabsl(f) > (inv_freq ? 1048576.0L : 256.0L)) return LWQ_ERR_INVALID_ARG;
+        r.turn[i] = turn_of(f);
     }
     *rope = r;
     return LWQ_OK;

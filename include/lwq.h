@@ -286,9 +286,10 @@ typedef struct {
  * elements from rot_dim on stay.
  *   LWQ_ROPE_HALF   pair i is elements (i, i + rot_dim / 2)
  *   LWQ_ROPE_PAIRS  pair i is elements (2 i, 2 i + 1)
- * Angles are kept as 64-bit fractions of a full turn, so that the product
- * with any 32-bit position is reduced exactly (cos and sin to about 2^-23,
- * however far the position). */
+ * Angles are kept as 64-bit fractions of a full turn (f_i / (2 pi) modulo 1,
+ * rounded to 2^-64), so that the product with any 32-bit position is reduced
+ * exactly: cos and sin to about 2^-22, however far the position and however
+ * large f_i. */
 #define LWQ_ROPE_HALF 0
 #define LWQ_ROPE_PAIRS 1
 typedef struct {
@@ -299,8 +300,10 @@ typedef struct {
 
 /* Fill *rope on the host (once; it holds no pointers and may be copied).
  *   rot_dim   a multiple of 16, 16 .. 128
- *   f_i       inv_freq[i] (rot_dim / 2 finite doubles below 2^20 in size), or,
- *             with inv_freq NULL, base^(-2 i / rot_dim), base > 0
+ *   f_i       inv_freq[i] (rot_dim / 2 finite doubles of at most 2^20 in size),
+ *             or, with inv_freq NULL, base^(-2 i / rot_dim), base > 0, in 64
+ *             bits, which is off by too much at far positions where it exceeds
+ *             256: refused, LWQ_ERR_INVALID_ARG
  *   axes      1 .. 4 position axes (3 for time, height and width); sections:
  *             how many consecutive pairs each axis turns, rot_dim / 2 in all
  *             (NULL with one axis)
