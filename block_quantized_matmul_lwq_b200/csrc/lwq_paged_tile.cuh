@@ -102,12 +102,12 @@ __device__ __forceinline__ int token_count(const PagedAttnArgs &a, int b) {
 struct RowSet {
     int b, tok0, n;     // sequence, its first token's row of q, its tokens
     int row0;           // first row of the pair among the sequence's n * G
-    int len, cap;
+    int len;            // the sequence's tokens in the cache, at most what its page table holds
 };
 // tokens seen before and at row r: -1 for a row that sees nothing, else the sequence's own tokens
 __device__ __forceinline__ int own_seen(const RowSet &s, int G, int r) {
     const long place = (long)s.len - s.n + r / G;
-    return place < 0 ? -1 : (int)(place + 1 < s.cap ? place + 1 : s.cap);
+    return place < 0 ? -1 : (int)(place + 1);
 }
 
 template <int D, int KT>
@@ -220,7 +220,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const int g = (int)(blockIdx.x % group) / ta.splits, split = (int)(blockIdx.x % ta.splits);
     const long pair = blockIdx.x / group;
     RowSet rs;
-    rs.cap = c.max_pages * c.page;
     long pl;
     if (ta.prefix_only) {
         rs.b = 0;
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
         rs.tok0 = first_token(a, rs.b);
         rs.n = token_count(a, rs.b);
-        rs.len = __ldg(c.lens + rs.b);
+        rs.len = min(__ldg(c.lens + rs.b), c.max_pages * c.page);
         pl = pairs_of(rs.n, a.G) - 1 - (pair - before);   // the rows that see most first
     }
     rs.row0 = (int)(pl * PAIR_ROWS);

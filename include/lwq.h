@@ -259,7 +259,9 @@ int lwq_attention_decode(int dtype, const void *q, const void *k, const void *v,
  *              that the call appends or attends with included, the shared
  *              prefix not.  0 (or less) is an empty sequence, e.g. a padded
  *              row of a captured batch.  The attention calls take a length
- *              beyond max_pages * page as that.
+ *              beyond max_pages * page as max_pages * page (so the last new
+ *              token sees all of the table's tokens, the one before it one
+ *              less); lwq_kv_append drops what lies beyond (below).
  *   prefix     [ceil(prefix_len / page)] int32, device: the pages of a prefix
  *              that every sequence begins with (a system prompt); NULL with
  *              prefix_len 0.  Token j of a sequence is then at position
