@@ -247,6 +247,17 @@ size_t tile_part_bytes(long pairs, int Hkv, int splits, int D) {
     return (size_t)pairs * Hkv * splits * PAIR_ROWS * part_stride(D) * sizeof(float);
 }
 
+// The most bytes that up to `pairs` pairs take: fewer pairs are cut into more parts (whole: pairs that are not cut have
+// partial results too).
+size_t tile_part_most(long pairs, int Hkv, long keys, int sms, int D, bool whole) {
+    size_t most = whole ? tile_part_bytes(pairs, Hkv, 1, D) : 0;
+    for (long p = 1; p <= pairs && p * Hkv * 2 <= sms; ++p) {   // (beyond, tile_splits is 1)
+        const size_t n = tile_part_bytes(p, Hkv, tile_splits(p, Hkv, keys, sms), D);
+        if (n > most) most = n;
+    }
+    return most;
+}
+
 // How a prefill call is divided.
 void prefill_plan(const lwq_paged *c, int T, int H, int sms, long *pairs, int *splits) {
     *pairs = tile_pairs(T, c->B, H / c->Hkv);
@@ -381,7 +392,9 @@ size_t lwq_attention_paged_workspace_size(const lwq_paged *cache, int H) {
     if (paged_sizes(cache, H)) return 0;
     int dev = 0, sms = 148;
     if (current_device(&dev) == LWQ_OK) sms = sm_count(dev);
-    return decode_space(cache, H, sms).total();
+    DecodeSpace s = decode_space(cache, H, sms);
+    if (cache->prefix_len > 0) s.prefix = tile_part_most(s.pairs, cache->Hkv, cache->prefix_len, sms, cache->D, true);
+    return s.total();
 }
 
 int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *out, int H, float scale,
@@ -429,10 +442,8 @@ size_t lwq_attention_prefill_workspace_size(const lwq_paged *cache, int T, int H
     if (paged_sizes(cache, H) || T <= 0) return 0;
     int dev = 0, sms = 148;
     if (current_device(&dev) == LWQ_OK) sms = sm_count(dev);
-    long pairs;
-    int splits;
-    prefill_plan(cache, T, H, sms, &pairs, &splits);
-    const size_t need = splits > 1 ? tile_part_bytes(pairs, cache->Hkv, splits, cache->D) : 0;
+    const size_t need = tile_part_most(tile_pairs(T, cache->B, H / cache->Hkv), cache->Hkv,
+                                       (long)cache->max_pages * cache->page + cache->prefix_len, sms, cache->D, false);
     return need < 256 ? 256 : need;
 }
 

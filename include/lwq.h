@@ -357,7 +357,8 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
  * are read once for the whole batch, as one matrix product over all B queries.
  * Needs the workspace of lwq_init: lwq_attention_paged_workspace_size bytes,
  * which depends on the sizes in *cache (its pointers are not read) and never
- * on the sequences' lengths; like lwq_matmul's, calls sharing it must be
+ * on the sequences' lengths, and does for every call with no more sequences,
+ * pages per sequence and prefix tokens; like lwq_matmul's, calls sharing it must be
  * ordered (one stream, or events).  lwq_attention_paged_workspace_size returns
  * 0 for invalid sizes.  The keys and values of live tokens must be finite.
  * Errors as lwq_kv_append's, LWQ_ERR_INVALID_ARG for a scale that is not finite
@@ -376,7 +377,9 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
  * sequence's later tokens must be finite too: a token's probability of 0 for
  * them multiplies their values.  Workspace and errors as
  * lwq_attention_paged; it is needed only when few tokens meet long caches
- * and the keys are split. */
+ * and the keys are split, and lwq_attention_prefill_workspace_size bytes do
+ * for every call with no more tokens, sequences, pages per sequence and prefix
+ * tokens. */
 size_t lwq_attention_prefill_workspace_size(const lwq_paged *cache, int T, int H);
 int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void *out, const int32_t *cu_tokens,
                           int T, int H, float scale, void *stream);
