@@ -185,7 +185,7 @@ cudaError_t launch_paged_decode_x(int dtype, const PagedPrefixArgs &k, cudaStrea
 
 // -------------------------------------------------------------- row tiles
 template <int XT, int D, int PARTS>
-int launch_paged_tile(const lwq_paged *c, PagedTileArgs &t, long pairs, cudaStream_t st) {
+int launch_paged_tile(const lwq_paged *c, PagedTileArgs &t, cudaStream_t st) {
     // three parts of a probability fit beside each other for 64 keys at a time
     constexpr int KT = PARTS == 3 ? 64 : 128;
     auto kern = paged_tile_kernel<XT, D, PARTS, KT>;
@@ -202,7 +202,7 @@ int launch_paged_tile(const lwq_paged *c, PagedTileArgs &t, long pairs, cudaStre
         if (encode_cached(r, &maps[i])) return LWQ_ERR_CUDA;
     }
     if (ensure_smem(reinterpret_cast<const void *>(kern), smem) != cudaSuccess) return LWQ_ERR_CUDA;
-    if (launch_k(kern, (int)(pairs * c->Hkv * t.splits), TILE_THREADS, smem, st, false, maps[0], maps[1], t) != cudaSuccess)
+    if (launch_k(kern, (int)(t.pairs * c->Hkv * t.splits), TILE_THREADS, smem, st, false, maps[0], maps[1], t) != cudaSuccess)
         return LWQ_ERR_CUDA;
     if (t.prefix_only || t.splits == 1) return LWQ_OK;
     return launch_k(paged_tile_combine_kernel<XT, D>, (int)(((long)t.a.T * t.a.H + 7) / 8), 256, 0, st, true, t) ==
@@ -213,13 +213,13 @@ int launch_paged_tile(const lwq_paged *c, PagedTileArgs &t, long pairs, cudaStre
 // The parts of a probability: see the kernel's header.  A prefix's partial results go on to other sums in fp32, but a
 // 16-bit result is no nearer for that.
 template <int D>
-int launch_paged_tile_x(const lwq_paged *c, PagedTileArgs &t, long pairs, cudaStream_t st) {
+int launch_paged_tile_x(const lwq_paged *c, PagedTileArgs &t, cudaStream_t st) {
     if (c->dtype == LWQ_ACT_F16)
-        return t.a.out16 ? launch_paged_tile<X_F16, D, 1>(c, t, pairs, st) : launch_paged_tile<X_F16, D, 2>(c, t, pairs, st);
-    return t.a.out16 ? launch_paged_tile<X_BF16, D, 1>(c, t, pairs, st) : launch_paged_tile<X_BF16, D, 3>(c, t, pairs, st);
+        return t.a.out16 ? launch_paged_tile<X_F16, D, 1>(c, t, st) : launch_paged_tile<X_F16, D, 2>(c, t, st);
+    return t.a.out16 ? launch_paged_tile<X_BF16, D, 1>(c, t, st) : launch_paged_tile<X_BF16, D, 3>(c, t, st);
 }
 
-PagedTileArgs paged_tile_args(const lwq_paged *c, const PagedAttnArgs &a, int splits, float *part) {
+PagedTileArgs paged_tile_args(const lwq_paged *c, const PagedAttnArgs &a, long pairs, int splits, float *part) {
     PagedTileArgs t;
     t.a = a;
     t.flip = a.qscale < 0.f;
@@ -227,6 +227,7 @@ PagedTileArgs paged_tile_args(const lwq_paged *c, const PagedAttnArgs &a, int sp
     if (t.a.qscale < 1e-30f) t.a.qscale = 1e-30f;   // scale 0: a masked score stays -inf, any other becomes 0
     t.part = part;
     t.splits = splits;
+    t.pairs = pairs;
     t.prefix_only = 0;
     t.total_rows = c->num_pages * c->Hkv * c->page;
     t.timeout_ns = kTimeoutNs;
@@ -424,10 +425,10 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
         k.splits = sp.splits;
         float *part = d.whole + sp.whole / sizeof(float);
         k.prefix = part;
-        PagedTileArgs t = paged_tile_args(cache, a, sp.splits, part);
+        PagedTileArgs t = paged_tile_args(cache, a, sp.pairs, sp.splits, part);
         t.prefix_only = 1;
-        if ((rc = cache->D == 64 ? launch_paged_tile_x<64>(cache, t, sp.pairs, st)
-                                 : launch_paged_tile_x<128>(cache, t, sp.pairs, st)))
+        if ((rc = cache->D == 64 ? launch_paged_tile_x<64>(cache, t, st)
+                                 : launch_paged_tile_x<128>(cache, t, st)))
             return rc;
         ++launches;
     }
@@ -461,10 +462,9 @@ int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void
     if ((double)pairs * cache->Hkv * splits > (double)kMaxIndex) return LWQ_ERR_UNSUPPORTED;
     void *ws;
     if ((rc = paged_workspace(dev, splits > 1 ? tile_part_bytes(pairs, cache->Hkv, splits, cache->D) : 0, &ws))) return rc;
-    PagedTileArgs t = paged_tile_args(cache, a, splits, static_cast<float *>(ws));
+    PagedTileArgs t = paged_tile_args(cache, a, pairs, splits, static_cast<float *>(ws));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if ((rc = cache->D == 64 ? launch_paged_tile_x<64>(cache, t, pairs, st) : launch_paged_tile_x<128>(cache, t, pairs, st)))
-        return rc;
+    if ((rc = cache->D == 64 ? launch_paged_tile_x<64>(cache, t, st) : launch_paged_tile_x<128>(cache, t, st))) return rc;
     t_last_launches = splits > 1 ? 2 : 1;
     return LWQ_OK;
 }

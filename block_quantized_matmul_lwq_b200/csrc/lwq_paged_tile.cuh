@@ -81,6 +81,7 @@ struct PagedTileArgs {
     PagedAttnArgs a;
     float *part;        // partial results [(pair * Hkv + g) * splits + s][256 rows], or null: write out
     int splits;
+    long pairs;         // of row tiles that the call has room for
     int prefix_only;    // the batch's queries (one row set of all T tokens) against the prefix alone
     int flip;           // negative scale: Q's signs are flipped and qscale is positive
     int total_rows;     // cache rows (num_pages Hkv page): the coordinate of a page that is not there
@@ -793,12 +794,14 @@ __global__ void __launch_bounds__(256) paged_tile_combine_kernel(const PagedTile
             break;
         }
     }
-    if (n == 0) {   // behind the last sequence (the wait all the same: this kernel may not end before the tiles')
+    const long ri = (long)(t - tok0) * a.G + hh % a.G;
+    const long pair = before + pairs_of(n, a.G) - 1 - ri / PAIR_ROWS;
+    // behind the last sequence, or of offsets that do not ascend, whose sequences overlap and have more pairs than there
+    // are partial results (the wait all the same: this kernel may not end before the tiles')
+    if (n == 0 || pair >= ta.pairs) {
         pdl_wait();
         return;
     }
-    const long ri = (long)(t - tok0) * a.G + hh % a.G;
-    const long pair = before + pairs_of(n, a.G) - 1 - ri / PAIR_ROWS;
     const int r = (int)(ri % PAIR_ROWS);
     pdl_wait();
     const float *p0 = ta.part + (((size_t)(pair * c.Hkv + g) * ta.splits) * PAIR_ROWS + r) * PS;
