@@ -68,6 +68,12 @@ bool overlap(const void *a, size_t an, const void *b, size_t bn) {
     return x < y + bn && y < x + an;
 }
 
+// [a, a + an) shares a byte with the cache's pages
+bool overlaps_cache(const lwq_paged *c, const void *a, size_t an) {
+    const size_t n = (size_t)c->num_pages * c->Hkv * c->page * c->D * 2;
+    return overlap(a, an, c->k, n) || overlap(a, an, c->v, n);
+}
+
 int rope_check(const lwq_rope *r, int D) {
     if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > D) return LWQ_ERR_UNSUPPORTED;
     if (r->layout != LWQ_ROPE_HALF && r->layout != LWQ_ROPE_PAIRS) return LWQ_ERR_UNSUPPORTED;
@@ -139,7 +145,8 @@ int paged_attn_args(const lwq_paged *c, int flags, const void *q, void *out, con
     a->qscale = scale * 1.4426950408889634f;   // log2(e): the kernels take exponentials as exp2
     if (!isfinite(a->qscale)) return LWQ_ERR_INVALID_ARG;
     const size_t n = (size_t)T * H * c->D;
-    if (overlap(q, 2 * n, out, (a->out16 ? 2 : 4) * n)) return LWQ_ERR_INVALID_ARG;
+    if (overlap(q, 2 * n, out, (a->out16 ? 2 : 4) * n) || overlaps_cache(c, out, (a->out16 ? 2 : 4) * n))
+        return LWQ_ERR_INVALID_ARG;
     return LWQ_OK;
 }
 
@@ -347,7 +354,7 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
         const size_t n = (size_t)T * H * D * 2;
         if (overlap(q_out, n, q, ((size_t)(T - 1) * ldq + (size_t)H * D) * es) ||
             overlap(q_out, n, k, ((size_t)(T - 1) * ldk + (size_t)cache->Hkv * D) * es) ||
-            overlap(q_out, n, v, ((size_t)(T - 1) * ldv + (size_t)cache->Hkv * D) * es))
+            overlap(q_out, n, v, ((size_t)(T - 1) * ldv + (size_t)cache->Hkv * D) * es) || overlaps_cache(cache, q_out, n))
             return LWQ_ERR_INVALID_ARG;
     }
     int dev;

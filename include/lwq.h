@@ -321,7 +321,9 @@ int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const do
  *              of Hkv heads, ldk and ldv apart.  (One fused projection y of
  *              [T][(H + 2 Hkv) D]: q = y, k = y + H D, v = y + (H + Hkv) D,
  *              all three strides (H + 2 Hkv) D.)
- *   q_out      [T][H][D] in the cache's dtype; may not overlap the inputs.
+ *   q_out      [T][H][D] in the cache's dtype; may not overlap the inputs or
+ *              the cache (nor may the rows of k and v overlap the places that
+ *              the call stores to).
  *              q and q_out may both be NULL: keys and values only (H is
  *              checked all the same).
  *   cu_tokens  [B + 1] int32, device, ascending from 0: sequence b's tokens
@@ -337,8 +339,9 @@ int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const do
  * call may not share a place in the cache (which of them stays would be open).
  * One kernel, no workspace.
  * Errors: LWQ_ERR_INVALID_ARG (sizes, NULL pointers, T != B without
- * cu_tokens, a stride below its row, q_out over an input), LWQ_ERR_UNSUPPORTED
- * (types, D, page, H / Hkv > 16, rot_dim > D, sizes past 31 bits),
+ * cu_tokens, a stride below its row, q_out over an input or the cache),
+ * LWQ_ERR_UNSUPPORTED (types, D, page, H / Hkv > 16, rot_dim > D, sizes past
+ * 31 bits),
  * LWQ_ERR_MISALIGNED (pointers or row strides that are not 16-byte multiples;
  * index arrays: 4 bytes), LWQ_ERR_CUDA. */
 int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const void *q, int64_t ldq, const void *k,
@@ -362,7 +365,7 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
  * ordered (one stream, or events).  lwq_attention_paged_workspace_size returns
  * 0 for invalid sizes.  The keys and values of live tokens must be finite.
  * Errors as lwq_kv_append's, LWQ_ERR_INVALID_ARG for a scale that is not finite
- * and for an out that overlaps q (there is no in-place form),
+ * and for an out that overlaps q (there is no in-place form) or the cache,
  * LWQ_ERR_NOT_INITIALIZED and LWQ_ERR_WORKSPACE_TOO_SMALL. */
 size_t lwq_attention_paged_workspace_size(const lwq_paged *cache, int H);
 int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *out, int H, float scale,
