@@ -77,8 +77,9 @@ class lwq_paged(ctypes.Structure):
     def __init__(self, act: int, k, v, tables, lens, *, B: int, Hkv: int, D: int, page: int, max_pages: int,
                  num_pages: int, prefix=None, prefix_len: int = 0):
         n = num_pages * Hkv * page * D
-        super().__init__(_tensor(k, "k", 2, n), _tensor(v, "v", 2, n), _tensor(tables, "tables", 4, B * max_pages),
-                         _tensor(lens, "lens", 4, B), _tensor(prefix, "prefix", 4, -(-prefix_len // max(page, 1))),
+        super().__init__(_tensor(k, "k", act, n), _tensor(v, "v", act, n), _tensor(tables, "tables", _INDEX, B * max_pages),
+                         _tensor(lens, "lens", _INDEX, B),
+                         _tensor(prefix, "prefix", _INDEX, -(-prefix_len // max(page, 1))),
                          prefix_len, act, B, Hkv, D, page, max_pages, num_pages)
         self.owners = (k, v, tables, lens, prefix)
         on = {p.get_device() for p in self.owners if hasattr(p, "get_device")}
@@ -87,6 +88,7 @@ class lwq_paged(ctypes.Structure):
         self.device = on.pop() if on else None
 
     at = property(ctypes.addressof)
+    owners, device = (), None       # of a copied descriptor: its tensors are not known
 
 
 class lwq_rope(ctypes.Structure):
@@ -168,27 +170,63 @@ def _ptr(p) -> int:
     return int(p.data_ptr())
 
 
-def _tensor(p, name: str, size: int, count: int = 0) -> int:
-    """_ptr of a tensor that a kernel will index: refused where it is on the host, holds elements of another size than
-    the call's, or, given a count, has fewer of them or is not contiguous."""
+_INDEX = "index"            # what _element_types has int32 arrays under, beside the activation codes
+_element_types = {}
+
+
+def _types(kind):
+    """The element types that a tensor of this kind (an activation code, or _INDEX) may have; None for a code that there is
+    not (the call itself refuses it).  Integers of 16 bits pass for 16-bit floats: the bits as they are."""
+    if not _element_types:
+        t = sys.modules["torch"]
+        bits = {getattr(t, n) for n in ("int16", "uint16") if hasattr(t, n)}
+        _element_types.update({LWQ_ACT_F32: {t.float32}, LWQ_ACT_F16: bits | {t.float16},
+                               LWQ_ACT_BF16: bits | {t.bfloat16},
+                               _INDEX: {getattr(t, n) for n in ("int32", "uint32") if hasattr(t, n)}})
+    return _element_types.get(kind)
+
+
+def _tensor(p, name: str, kind, count: int = 0, device=None) -> int:
+    """_ptr of a tensor that a kernel will index: refused where it is on the host or on another device than the cache's,
+    has another element type than the call's, or, given a count, has fewer elements or is not contiguous."""
     if p is None or p.__class__ is int:
         return p or 0
     try:
-        ok = p.is_cuda and p.element_size() == size and (not count or (p.numel() >= count and p.is_contiguous()))
+        on, types = p.get_device(), _element_types.get(kind) or _types(kind)
+        if ((on == device if device is not None else on >= 0) and (types is None or p.dtype in types)
+                and (not count or p.numel() >= count and p.is_contiguous())):
+            return p.data_ptr()
     except AttributeError:      # a pointer of another kind
         return _ptr(p)
-    if not ok:
-        raise ValueError(f"{name}: {count or ''} elements of {size} bytes on the GPU{' in one piece' if count else ''} "
-                         f"are needed, not {tuple(p.shape)} of {p.dtype} on {p.device} with strides {p.stride()}")
-    return p.data_ptr()
+    raise ValueError(f"{name}: {f'{count} elements in one piece' if count else 'elements'} of "
+                     f"{' or '.join(sorted(str(t) for t in _types(kind) or ()))} on "
+                     f"{'the GPU' if device is None else f'cuda:{device}'} are needed, not {tuple(p.shape)} of {p.dtype} on "
+                     f"{p.device} with strides {p.stride()}")
 
 
-def _same_device(cache, p) -> None:
-    """The cache's tensors, p and the current device (on which the call launches) are one."""
-    if cache.device is not None and hasattr(p, "get_device"):
-        if not cache.device == p.get_device() == sys.modules["torch"].cuda.current_device():
-            raise ValueError(f"the cache is on cuda:{cache.device}, the call's tensors on {p.device}, the current device "
-                             f"is cuda:{sys.modules['torch'].cuda.current_device()}")
+def _reaches(*rows) -> None:
+    """Each (tensor, name, pointer, bytes from there) ends within its tensor's memory (mostly one tensor's for all)."""
+    base = end = 0
+    for p, name, at, nbytes in rows:
+        if at and not (base <= at and at + nbytes <= end) and hasattr(p, "untyped_storage"):
+            s = p.untyped_storage()
+            base = s.data_ptr()
+            end = base + s.nbytes()
+            if at + nbytes > end:
+                raise ValueError(f"{name}: its rows end {at + nbytes - end} bytes behind the tensor's memory")
+
+
+_current = None                 # torch.cuda.current_device
+
+
+def _current_device(cache) -> None:
+    """The device of the cache's tensors is the current one, on which the call launches."""
+    global _current
+    if cache.device is not None:
+        if _current is None:
+            _current = sys.modules["torch"].cuda.current_device
+        if _current() != cache.device:
+            raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{_current()}")
 
 
 def _stream(s) -> int:
@@ -296,13 +334,17 @@ def lwq_rope_init(rot_dim: int, base: float = 10000.0, layout: int = LWQ_ROPE_HA
 def lwq_kv_append(cache: lwq_paged, rope, src: int, q, ldq: int, k, ldk: int, v, ldv: int, q_out, T: int, H: int,
                   cu_tokens=None, positions=None, stream=None) -> None:
     """Rotate q and k by position (rope None: not) and store k and v in the cache (see include/lwq.h)."""
-    es = 4 if src == LWQ_ACT_F32 else 2
-    _same_device(cache, k)
-    _check(_lib.lwq_kv_append(cache.at, None if rope is None else rope.at, src, _tensor(q, "q", es), ldq,
-                              _tensor(k, "k", es), ldk, _tensor(v, "v", es), ldv,
-                              _tensor(q_out, "q_out", 2, T * H * cache.D), _tensor(cu_tokens, "cu_tokens", 4),
-                              _tensor(positions, "positions", 4, T * (1 if rope is None else rope.axes)), T, H,
-                              _stream(stream)), "lwq_kv_append")
+    on, D, last, es = cache.device, cache.D, T - 1, 4 if src == LWQ_ACT_F32 else 2
+    n = cache.Hkv * D
+    qp, kp, vp = _tensor(q, "q", src, 0, on), _tensor(k, "k", src, 0, on), _tensor(v, "v", src, 0, on)
+    _reaches((v, "v", vp, (last * ldv + n) * es), (k, "k", kp, (last * ldk + n) * es),
+             (q, "q", qp, (last * ldq + H * D) * es))
+    out = _tensor(q_out, "q_out", cache.dtype, T * H * D, on)
+    cu = _tensor(cu_tokens, "cu_tokens", _INDEX, cache.B + 1, on)
+    pos = _tensor(positions, "positions", _INDEX, T * (1 if rope is None else rope.axes), on)
+    _current_device(cache)
+    _check(_lib.lwq_kv_append(cache.at, None if rope is None else rope.at, src, qp, ldq, kp, ldk, vp, ldv, out, cu, pos, T,
+                              H, _stream(stream)), "lwq_kv_append")
 
 
 def lwq_attention_paged_workspace_size(cache: lwq_paged, H: int) -> int:
@@ -311,11 +353,11 @@ def lwq_attention_paged_workspace_size(cache: lwq_paged, H: int) -> int:
 
 def lwq_attention_paged(cache: lwq_paged, q, out, H: int, scale: float, flags: int = 0, stream=None) -> None:
     """Decode attention, one query token per sequence, over the paged cache and its shared prefix."""
-    n = cache.B * H * cache.D
-    _same_device(cache, q)
-    _check(_lib.lwq_attention_paged(cache.at, flags, _tensor(q, "q", 2, n),
-                                    _tensor(out, "out", 2 if flags & LWQ_FLAG_OUT16 else 4, n), H, float(scale),
-                                    _stream(stream)), "lwq_attention_paged")
+    n, on = cache.B * H * cache.D, cache.device
+    ptrs = (_tensor(q, "q", cache.dtype, n, on),
+            _tensor(out, "out", cache.dtype if flags & LWQ_FLAG_OUT16 else LWQ_ACT_F32, n, on))
+    _current_device(cache)
+    _check(_lib.lwq_attention_paged(cache.at, flags, *ptrs, H, float(scale), _stream(stream)), "lwq_attention_paged")
 
 
 def lwq_attention_prefill_workspace_size(cache: lwq_paged, T: int, H: int) -> int:
@@ -325,9 +367,10 @@ def lwq_attention_prefill_workspace_size(cache: lwq_paged, T: int, H: int) -> in
 def lwq_attention_prefill(cache: lwq_paged, q, out, cu_tokens, T: int, H: int, scale: float, flags: int = 0,
                           stream=None) -> None:
     """Causal attention of the batch's new tokens over the cache that already holds them."""
-    n = T * H * cache.D
-    _same_device(cache, q)
-    _check(_lib.lwq_attention_prefill(cache.at, flags, _tensor(q, "q", 2, n),
-                                      _tensor(out, "out", 2 if flags & LWQ_FLAG_OUT16 else 4, n),
-                                      _tensor(cu_tokens, "cu_tokens", 4, cache.B + 1), T, H, float(scale),
-                                      _stream(stream)), "lwq_attention_prefill")
+    n, on = T * H * cache.D, cache.device
+    ptrs = (_tensor(q, "q", cache.dtype, n, on),
+            _tensor(out, "out", cache.dtype if flags & LWQ_FLAG_OUT16 else LWQ_ACT_F32, n, on),
+            _tensor(cu_tokens, "cu_tokens", _INDEX, cache.B + 1, on))
+    _current_device(cache)
+    _check(_lib.lwq_attention_prefill(cache.at, flags, *ptrs, T, H, float(scale), _stream(stream)),
+           "lwq_attention_prefill")
