@@ -19,7 +19,9 @@ batches) under "attention".
 
 Under torchrun every rank runs the same workload on its own GPU (the path
 has no exchange step: replicas, weak scaling) and rank 0 prints one JSON line
-with the max-over-ranks time.
+with the max-over-ranks time.  The line sums up what is measured beside the
+headline; the whole record, each call and sweep point of it, is a line of JSON
+on stderr.
 """
 
 from __future__ import annotations
@@ -748,11 +750,28 @@ def run_gpu_arm(args):
             "host_enqueue": host, "sweep": sweep,
             "device_error": err,
         }
-        print(json.dumps(line), flush=True)
+        print(json.dumps({"record": line}), file=sys.stderr, flush=True)
+        print(json.dumps(short_record(line)), flush=True)
     if dist_on:
         dist.barrier()
         dist.destroy_process_group()
     lwq.lwq_shutdown()
+
+
+def short_record(record: dict) -> dict:
+    """The record as the one line on stdout: the headline whole, of the other measurements what sums them up, so that the
+    line stays under 8000 characters (a reader that keeps the end of a long output keeps all of it)."""
+    line = dict(record)
+    line["workloads"] = {name: {k: v for k, v in w.items() if k not in ("per_call", "clocks", "steps")}
+                         for name, w in record["workloads"].items()}
+    if record.get("attention"):
+        line["attention"] = {name: {k: v for k, v in a.items() if isinstance(v, (int, float))}
+                             for name, a in record["attention"].items()}
+    if record.get("sweep"):
+        fracs = sorted(p["frac"] for p in record["sweep"]["points"])
+        line["sweep"] = {"frac": record["sweep"]["frac"], "points": len(fracs), "frac_least": fracs[0],
+                         "frac_median": fracs[len(fracs) // 2], "frac_most": fracs[-1]}
+    return line
 
 
 def run_sweep(args):
