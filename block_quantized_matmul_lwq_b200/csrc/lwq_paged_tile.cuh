@@ -27,7 +27,7 @@
 // The probabilities are PARTS 16-bit numbers each.  A 16-bit result takes one
 // part (off by half a step of that type per key, like the result's own
 // rounding); an fp32 result takes two in fp16 (22 bits; fp16's parts end at
-// 2^-24, whatever the probability, so they are taken of 2^11 to 2^15 p), three
+// 2^-24, whatever the probability, so they are taken of 2^10 to 2^15 p), three
 // in bf16 (24).
 // The tensor cores truncate what they add to O, which pulls every sum towards
 // zero by about 2^-23 per product of 16 keys; for an fp32 result O therefore
@@ -64,16 +64,17 @@ constexpr uint32_t TILE_TMEM_COLS = 512;
 // taken anew they begin at 2^LIFT, and until one would pass 2^ROOM a larger score changes nothing.
 //   bf16   has fp32's range: 0 and 8.
 //   fp16   ends at 2^-24 below and at 65504 above: ROOM is 15, the half that stays free being for the rounding of
-//          exponents up to EXACT in size.  Begun at 2^11, a row's weights are off by less than 2^-36 of its largest.
-//          Begun at 2^13 they outgrow the room so often that a prompt of 8192 tokens takes 1105 us instead of 915 (fp32
-//          results; 16-bit: 515 and 480).  But a key that stands alone above the tile's others by more than ALONE (an
-//          attention sink: nothing follows that comes near it) begins at 2^15, and they are off by 2^-40 of it: there
-//          the others' weights may be all that the result is made of, while without such a key weights within 2^-8 of
-//          the largest outweigh what is lost.  Beyond EXACT, where 15 would be lost in the rounding of the maximum
-//          itself, 0 and 2: scores of up to 2^27, off by up to 8 from their maximum, stay in the type.
+//          exponents up to EXACT in size.  Begun at 2^10, a row's weights are off by less than 2^-35 of its largest.
+//          Higher up they outgrow the room too often (fp32 results: at 2^11 ragged prompts take 80 to 84 us instead of
+//          76.6, at 2^13 a prompt of 8192 tokens 1105 instead of 930).  But a key that stands alone above the tile's
+//          others by more than ALONE (an attention sink: nothing follows that comes near it) begins at 2^15, and they
+//          are off by 2^-40 of it: there the others' weights may be all that the result is made of, while without such
+//          a key weights within 2^-8 of the largest outweigh what is lost.  Beyond EXACT, where 15 would be lost in the
+//          rounding of the maximum itself, 0 and 2: scores of up to 2^27, off by up to 8 from their maximum, stay in
+//          the type.
 template <int XT>
 struct TileRange {
-    static constexpr float LIFT = XT == X_F16 ? 11.f : 0.f, ROOM = XT == X_F16 ? 15.f : 8.f;
+    static constexpr float LIFT = XT == X_F16 ? 10.f : 0.f, ROOM = XT == X_F16 ? 15.f : 8.f;
     static constexpr float ALONE = 8.f, ALONE_LIFT = 15.f, EXACT = 4194304.f, FAR_ROOM = 2.f;
 };
 
