@@ -707,10 +707,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (mine > 0 && ok) ok = warp_wait(&o_full[t], 0);
         tc_fence_after();
         if (ok) {
-            if (ta.part && live) *reinterpret_cast<float2 *>(row32 - 4) = make_float2(m, l);
+            // (scores that are not numbers leave no maximum: the merge is to see their sum, not to take the row as empty)
+            if (ta.part && live) *reinterpret_cast<float2 *>(row32 - 4) = make_float2(l == l ? m : 0.f, l);
             const bool more = mine > (PARTS > 1 ? FRESH : RELIEF);   // sums were kept
             const float fk = more && kept != -INFINITY ? ex2(kept - m) * unit : 0.f;
-            const float inv = ta.part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+            const float inv = ta.part ? 1.f : 1.f / l;
 #pragma unroll
             for (int x0 = 0; x0 < D; x0 += 32) {
                 uint32_t o[32];
@@ -736,7 +737,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     }
                 }
 #pragma unroll
-                for (int x = 0; x < 32; ++x) f[x] = l > 0.f ? f[x] * inv : 0.f;
+                for (int x = 0; x < 32; ++x) f[x] = l == 0.f ? 0.f : f[x] * inv;   // (a row that saw nothing)
                 if (!ta.part && a.out16) {
                     uint16_t *dst = static_cast<uint16_t *>(a.out) + at + x0;
 #pragma unroll
@@ -824,7 +825,7 @@ __global__ void __launch_bounds__(256) paged_tile_combine_kernel(const PagedTile
         for (int u = 0; u < U; ++u) merge_part(M, L, A, mv[u], lv[u], av[u]);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) store_out<XT>(a, (size_t)w * D + 32 * e + lane, L > 0.f ? A[e] / L : 0.f);
+    for (int e = 0; e < E; ++e) store_out<XT>(a, (size_t)w * D + 32 * e + lane, L == 0.f ? 0.f : A[e] / L);
 }
 
 }  // namespace lwq
