@@ -51,7 +51,7 @@ __device__ __forceinline__ size_t cache_row(const PagedArgs &c, int p, int g, in
 // warp decides anything per head.  A block is one token's warps (up to 8: 40
 // rotated and 8 other heads of 128 take 6), which share the (cos, sin) of the
 // token's pairs: computed per warp they were half of all instructions (7776
-// tokens, 48 heads of 128: 58.5 us, and 51 us shared: 5.6 TB/s).
+// tokens, 48 heads of 128: 58.5 us, and 52 to 53 us shared: 5.4 TB/s).
 //
 // The angle position * f is kept in turns as a 64-bit fraction: the low 64 bits
 // of position * turn are the exact product modulo one turn, and their top 32

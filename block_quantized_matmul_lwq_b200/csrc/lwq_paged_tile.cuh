@@ -32,8 +32,9 @@
 // The tensor cores truncate what they add to O, which pulls every sum towards
 // zero by about 2^-23 per product of 16 keys; for an fp32 result O therefore
 // starts anew every 1024 keys and the sums so far are kept, in rounded fp32,
-// in the row's place in the output (or among the partial results): 1 to 3e-6 of
-// the result at any length.  For a 16-bit result it is relieved every 16384 keys
+// in the row's place in the output (or among the partial results): at any length
+// 2e-6 (bf16) and 7e-6 (fp16) of a result whose values have one sign, 1 to 2e-6
+// of sum p |v| otherwise.  For a 16-bit result it is relieved every 16384 keys
 // in fp16, every 32768 in bf16 (1e-4 and 2e-4 of the result, a fifth and a
 // twentieth of a half step; 131072 keys left to one accumulator took 8e-4, nearly
 // two half steps of fp16): the row's place in the output takes the sums so far
@@ -42,12 +43,14 @@
 // time costs a CTA about 10 us (16384 tokens relieved every 8192 keys took 2.10
 // ms, never 2.01), so it is not done more often.
 //
-// Measured (32 query and 8 kv heads of 128, bf16): a prompt of 8192 tokens in
-// 455 us, 1.21 PFLOP/s, 0.72 of what a large matrix product reaches in a burst;
-// 16384 tokens at 1.33 PFLOP/s; 8192 with an fp32 result in 922 us.  A key tile of
-// both row tiles takes about 3000 cycles, of which the tensor core works 2050:
-// one row tile's softmax (2000 cycles) and the products behind it (900) form a
-// chain, and 7 us of a CTA's life are its start and end.
+// Measured (32 query and 8 kv heads of 128, bf16, other inputs each time): a
+// prompt of 8192 tokens in 515 to 535 us, 1.03 to 1.07 PFLOP/s, 0.61 to 0.64 of
+// what a large matrix product reaches in a burst (0.74 to 0.77 of what it
+// sustains); 16384 tokens in 1.94 ms, 1.13 PFLOP/s; 8192 with an fp32 result in
+// 1.06 ms, fp16 0.93.  A key tile of both row tiles takes about 3000 cycles, of
+// which the tensor core works 2050: one row tile's softmax (2000 cycles) and the
+// products behind it (900) form a chain, and 7 us of a CTA's life are its start
+// and end.
 #pragma once
 
 #include "lwq_paged_decode.cuh"

@@ -341,29 +341,41 @@ int lwq_rope_init(lwq_rope *rope, int rot_dim, int layout, double base, const do
  * Errors: LWQ_ERR_INVALID_ARG (sizes, NULL pointers, T != B without
  * cu_tokens, a stride below its row, q_out over an input or the cache),
  * LWQ_ERR_UNSUPPORTED (types, D, page, H / Hkv > 16, rot_dim > D, sizes past
- * 31 bits),
- * LWQ_ERR_MISALIGNED (pointers or row strides that are not 16-byte multiples;
- * index arrays: 4 bytes), LWQ_ERR_CUDA. */
+ * 31 bits), LWQ_ERR_MISALIGNED (pointers or row strides that are not 16-byte
+ * multiples; index arrays: 4 bytes), LWQ_ERR_CUDA. */
 int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const void *q, int64_t ldq, const void *k,
                   int64_t ldk, const void *v, int64_t ldv, void *q_out, const int32_t *cu_tokens,
                   const int32_t *positions, int T, int H, void *stream);
 
-/* Flag of the two attention calls below: out in the cache's 16-bit type,
- * rounded once, instead of fp32. */
+/* Flag of the two attention calls below: out in the cache's 16-bit type
+ * instead of fp32.
+ * Precision, relative to sum_j softmax(s)_j |v_j| and beside the rounding of
+ * the scores in fp32:
+ *   fp32 results     1e-6 from lwq_attention_paged's own tokens; up to 1e-5 from
+ *                    a prefix's and in lwq_attention_prefill, at any length
+ *   16-bit results   half a step of the type for the result's rounding.  A
+ *                    prefix's tokens and lwq_attention_prefill take each weight
+ *                    softmax(s)_j rounded to the type as well: up to half a step
+ *                    more, as much again as the result's rounding on average
+ *                    (ask for fp32 where that is too much)
+ * In an fp16 cache each weight is off by up to 2^-35 of its row's largest
+ * besides (lwq_attention_paged's own tokens, and where one key stands alone far
+ * above the others: 2^-40).  Scores may be 1e8 in size. */
 #define LWQ_FLAG_OUT16 0x4000
 
 /* Decode attention over the paged cache: q [B][H][D] in the cache's dtype,
  * out [B][H][D] fp32 (or 16-bit, flags above).  Query h reads kv head
  * h / (H / Hkv), H / Hkv at most 16.  With s_j = scale * (q . k_j) over the
  * prefix_len + lens[b] tokens of sequence b,  out = sum_j softmax(s)_j v_j;
- * a sequence with no token at all gets zeros.  The prefix's keys and values
- * are read once for the whole batch, as one matrix product over all B queries.
+ * a sequence with no token at all gets zeros, a query that holds NaN gets NaN.
+ * The prefix's keys and values are read once for the whole batch, as one matrix
+ * product over all B queries.
  * Needs the workspace of lwq_init: lwq_attention_paged_workspace_size bytes,
  * which depends on the sizes in *cache (its pointers are not read) and never
- * on the sequences' lengths, and does for every call with no more sequences,
- * pages per sequence and prefix tokens; like lwq_matmul's, calls sharing it must be
- * ordered (one stream, or events).  lwq_attention_paged_workspace_size returns
- * 0 for invalid sizes.  The keys and values of live tokens must be finite.
+ * on the sequences' lengths, and is enough for every call with no more
+ * sequences, pages per sequence and prefix tokens.  Like lwq_matmul's, calls
+ * sharing it must be ordered (one stream, or events).
+ * lwq_attention_paged_workspace_size returns 0 for invalid sizes.  The keys and values of live tokens must be finite.
  * Errors as lwq_kv_append's, LWQ_ERR_INVALID_ARG for a scale that is not finite
  * and for an out that overlaps q (there is no in-place form) or the cache,
  * LWQ_ERR_NOT_INITIALIZED and LWQ_ERR_WORKSPACE_TOO_SMALL. */
@@ -380,9 +392,9 @@ int lwq_attention_paged(const lwq_paged *cache, int flags, const void *q, void *
  * sequence's later tokens must be finite too: a token's probability of 0 for
  * them multiplies their values.  Workspace and errors as
  * lwq_attention_paged; it is needed only when few tokens meet long caches
- * and the keys are split, and lwq_attention_prefill_workspace_size bytes do
- * for every call with no more tokens, sequences, pages per sequence and prefix
- * tokens. */
+ * and the keys are split, and lwq_attention_prefill_workspace_size bytes are
+ * enough for every call with no more tokens, sequences, pages per sequence and
+ * prefix tokens. */
 size_t lwq_attention_prefill_workspace_size(const lwq_paged *cache, int T, int H);
 int lwq_attention_prefill(const lwq_paged *cache, int flags, const void *q, void *out, const int32_t *cu_tokens,
                           int T, int H, float scale, void *stream);
