@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -231,7 +232,8 @@ PagedTileArgs paged_tile_args(const lwq_paged *c, const PagedAttnArgs &a, long p
     t.a = a;
     t.flip = a.qscale < 0.f;
     t.a.qscale = fabsf(a.qscale);
-    if (t.a.qscale < 1e-30f) t.a.qscale = 1e-30f;   // scale 0: a masked score stays -inf, any other becomes 0
+    // scale 0: a masked score stays -inf, any other becomes 0 (below 4, however large the product of query and key)
+    if (t.a.qscale < FLT_MIN) t.a.qscale = FLT_MIN;
     t.part = part;
     t.splits = splits;
     t.pairs = pairs;

@@ -75,3 +75,21 @@ def test_raw_storage(dev):                                         # noqa: F811
     lwq.lwq_attention_paged(raw, p.q.view(torch.int16), out, 4, p.scale, flags=lwq.LWQ_FLAG_OUT16)
     torch.cuda.synchronize(dev)
     assert_attention(p, out.view(torch.bfloat16), False, True)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-33, -1e-33])
+@pytest.mark.parametrize("where", ["prefix", "prefill"])
+def test_small_scales_with_large_products(dev, where, scale):      # noqa: F811
+    """Queries and keys of 1e15 in size: products near 1e31 times a scale of 0 or 1e-33."""
+    p = Problem(dev, "bf16", [100, 7], 4, 2, 64, 16, new=[90, 7] if where == "prefill" else None,
+                prefix=0 if where == "prefill" else 200, seed=6)
+    p.q *= 1e15
+    p.kc *= 1e15
+    p.scale = scale
+    out = torch.zeros((p.T, 4, 64), device=dev)
+    if where == "prefill":
+        lwq.lwq_attention_prefill(p.cache(), p.q, out, p.cu_d, p.T, 4, scale)
+    else:
+        lwq.lwq_attention_paged(p.cache(), p.q, out, 4, scale)
+    torch.cuda.synchronize(dev)
+    assert_attention(p, out, where == "prefill")
