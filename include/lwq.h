@@ -375,7 +375,8 @@ int lwq_kv_append(const lwq_paged *cache, const lwq_rope *rope, int src, const v
  * on the sequences' lengths, and is enough for every call with no more
  * sequences, pages per sequence and prefix tokens.  Like lwq_matmul's, calls
  * sharing it must be ordered (one stream, or events).
- * lwq_attention_paged_workspace_size returns 0 for invalid sizes.  The keys and values of live tokens must be finite.
+ * lwq_attention_paged_workspace_size returns 0 for invalid sizes.  The keys and
+ * values of live tokens must be finite.
  * Errors as lwq_kv_append's, LWQ_ERR_INVALID_ARG for a scale that is not finite
  * and for an out that overlaps q (there is no in-place form) or the cache,
  * LWQ_ERR_NOT_INITIALIZED and LWQ_ERR_WORKSPACE_TOO_SMALL. */
